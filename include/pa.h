@@ -25,6 +25,10 @@
  *   - Optional sliding window of W tokens (ldpk §5.3): each query attends only the most
  *     recent W positions, its own included, and blocks that fall wholly before the window
  *     go back to the pool (pa_bm_slide_window), so a sequence holds O(W) cache.
+ *   - Optional anchors beside the window: the first A tokens stay visible to every query
+ *     (pa_decode_attention_anchored, pa_prefill_attention_anchored), and their blocks stay in the
+ *     pool (pa_bm_slide_window_anchored).  显存账本 §七 keeps the first tokens because attention gathers
+ *     there; dropped from a window they take most of the softmax mass with them.
  *   - Sequences that share a prompt prefix point their tables at one copy of its whole blocks
  *     (AI内存系统 §3.1, §3.3); pa_decode_attention_shared attends those blocks once for all of
  *     them and merges that part with each sequence's own positions.
@@ -260,6 +264,29 @@ pa_status pa_decode_attention_shared(const pa_cache_desc* desc, void* out, const
                                      int32_t* err_flag, void* stream);
 
 /* ---------------------------------------------------------------------------------
+ * Decode attention over a sliding window and the first tokens (ldpk §5.3 window; 显存账本 §七: the
+ * first tokens gather attention whatever they hold).  As pa_decode_attention with
+ * desc->sliding_window = W, except that positions t < num_anchor (the anchors) stay visible: the
+ * query of a ctx-token sequence attends t < min(num_anchor, ctx) and max(0, ctx-W) .. ctx-1.  An
+ * anchor below desc->num_sink is read from the sink buffers, the others from the cache.  Only the
+ * table entries of blocks that hold an attended position not below num_sink are read, or one that
+ * lies in the window: after pa_bm_slide_window_anchored every other entry may be -1.  With
+ * sliding_window == 0, or num_anchor == 0, the call is pa_decode_attention.
+ *   num_anchor    >= 0; PA_ERR_INVALID_ARG otherwise
+ *   workspace     at least pa_decode_anchored_workspace_size(desc, max_context_len, partition_size,
+ *                 num_anchor) bytes, 256-byte aligned, scratch for this call only.  The size is 0
+ *                 when an argument is invalid.
+ * Every cache kind; other arguments, device errors and host errors as pa_decode_attention. */
+size_t pa_decode_anchored_workspace_size(const pa_cache_desc* desc, int max_context_len, int partition_size,
+                                         int num_anchor);
+
+pa_status pa_decode_attention_anchored(const pa_cache_desc* desc, void* out, const void* q,
+                                       const void* k_cache, const void* v_cache,
+                                       const int32_t* block_tables, const int32_t* context_lens,
+                                       int max_context_len, float scale, int partition_size, int num_anchor,
+                                       void* workspace, size_t workspace_bytes, int32_t* err_flag, void* stream);
+
+/* ---------------------------------------------------------------------------------
  * Chunked-prefill (extend) attention over the paged cache (ldpk §2.2: under the causal mask the
  * query of position i attends to positions up to i; ldpk §7: long prompts are prefilled in
  * chunks).  Sequence s contributes the query rows q_start[s] .. q_start[s+1]-1 of q: they are its
@@ -345,6 +372,36 @@ pa_status pa_prefill_step_ws(const pa_cache_desc* desc, void* out, const void* q
                              const int32_t* context_lens, int max_query_len, int max_context_len,
                              float scale, void* workspace, size_t workspace_bytes, int32_t* err_flag,
                              void* stream);
+
+/* Chunked-prefill attention over a sliding window and the first tokens (as
+ * pa_decode_attention_anchored): as pa_prefill_attention with desc->sliding_window = W, except that
+ * positions t < num_anchor stay visible: the query at position p attends t <= p with t < num_anchor
+ * or t > p-W.  An anchor below desc->num_sink is read from the sink buffers.  Table entries of blocks
+ * that hold neither an anchor nor a position of some query's window are never read (they may be -1
+ * after pa_bm_slide_window_anchored).  With sliding_window == 0, or num_anchor == 0, the result is
+ * pa_prefill_attention's.
+ *   num_anchor        >= 0
+ *   scale             finite and > 0 (the tensor-core kernel takes a row's maximum before it scales)
+ *   max_context_len   bounds every context_lens[s]; 0 <= max_context_len <= max_blocks_per_seq*16.
+ *   workspace         at least pa_prefill_anchored_workspace_size(...) bytes, 256-byte aligned,
+ *                     scratch for this call only: caches that are decoded (8-bit, per-token-scaled,
+ *                     INT4, with sinks) are decoded into it block by block, once, as by
+ *                     pa_prefill_attention_ws, but only the blocks that the chunk can attend, so its
+ *                     size goes with W + max_query_len + num_anchor, not with the context.  The size
+ *                     is 0 when the call needs none (as pa_prefill_workspace_size; workspace may then
+ *                     be NULL) or an argument is invalid.
+ * A sequence that breaks pa_prefill_attention's rules, or (with a workspace) has a context beyond
+ * max_context_len, sets PA_EFLAG_CTX_OVERFLOW and gets zero rows; other rules, device errors and
+ * host errors as pa_prefill_attention_ws. */
+size_t pa_prefill_anchored_workspace_size(const pa_cache_desc* desc, int max_query_len, int max_context_len,
+                                          int num_anchor);
+
+pa_status pa_prefill_attention_anchored(const pa_cache_desc* desc, void* out, const void* q,
+                                        const void* k_cache, const void* v_cache,
+                                        const int32_t* block_tables, const int32_t* q_start,
+                                        const int32_t* context_lens, int max_query_len, int max_context_len,
+                                        float scale, int num_anchor, void* workspace, size_t workspace_bytes,
+                                        int32_t* err_flag, void* stream);
 
 /* Allocation-free decode attention.  The pages have no counterpart to this entry point: it is
  * pa_decode_attention for callers that cannot allocate device memory when they call it, for
@@ -446,6 +503,13 @@ pa_status pa_bm_prepare_step(pa_bm* bm, int32_t* block_tables, int num_seqs,
  * sequences before it keep their changes). */
 int pa_bm_slide_window(pa_bm* bm, int32_t* block_tables, int num_seqs, int max_blocks_per_seq,
                        const int32_t* context_lens, int window, int* n_freed);
+
+/* The same release, keeping the blocks of the anchors: logical blocks 0 .. ceil(num_anchor/16) - 1
+ * are left alone (pa_decode_attention_anchored and pa_prefill_attention_anchored read them).
+ * Anchors that live in the sink buffers need no block: pass 0 when num_anchor <= num_sink.
+ * num_anchor == 0 is pa_bm_slide_window; num_anchor < 0 is an invalid argument (-1). */
+int pa_bm_slide_window_anchored(pa_bm* bm, int32_t* block_tables, int num_seqs, int max_blocks_per_seq,
+                                const int32_t* context_lens, int window, int num_anchor, int* n_freed);
 
 /* ---------------------------------------------------------------------------------
  * Prefix cache ("大模型推理KV Cache显存优化：从PagedAttention到AI内存系统演进", prefix-cache

@@ -14,4 +14,5 @@ float8 cast, numpy's round-half-even) and brute force on tiny inputs.
 """
 
 from .paged_kv import *  # noqa: F401,F403
+from .bounded import *  # noqa: F401,F403
 from .prefix_cache import *  # noqa: F401,F403

@@ -172,8 +172,14 @@ pa_status pa_bm_prepare_step(pa_bm* bm, int32_t* block_tables, int num_seqs,
 
 int pa_bm_slide_window(pa_bm* bm, int32_t* block_tables, int num_seqs, int max_blocks_per_seq,
                        const int32_t* context_lens, int window, int* n_freed) {
+  return pa_bm_slide_window_anchored(bm, block_tables, num_seqs, max_blocks_per_seq, context_lens, window, 0, n_freed);
+}
+
+int pa_bm_slide_window_anchored(pa_bm* bm, int32_t* block_tables, int num_seqs, int max_blocks_per_seq,
+                                const int32_t* context_lens, int window, int num_anchor, int* n_freed) {
   if (n_freed) *n_freed = 0;
-  if (!bm || !block_tables || !context_lens || num_seqs < 0 || max_blocks_per_seq <= 0 || window < 0)
+  if (!bm || !block_tables || !context_lens || num_seqs < 0 || max_blocks_per_seq <= 0 || window < 0 ||
+      num_anchor < 0)
     return -1;
   if (window == 0) return 0;
   std::lock_guard<std::mutex> g(bm->mu);
@@ -183,7 +189,8 @@ int pa_bm_slide_window(pa_bm* bm, int32_t* block_tables, int num_seqs, int max_b
     if (c <= window) continue;
     const int n = std::min((c - window) / bm->block_size, max_blocks_per_seq);
     int32_t* row = block_tables + (size_t)s * max_blocks_per_seq;
-    for (int lb = 0; lb < n; ++lb) {
+    const int first = num_anchor / bm->block_size + (num_anchor % bm->block_size ? 1 : 0);
+    for (int lb = first; lb < n; ++lb) {
       const int b = row[lb];
       if (b < 0) continue;
       if (!bm->valid_allocated(b)) {

@@ -7,7 +7,9 @@
 // (ldpk §4.3; 显存账本 §四 locate()).  8-bit caches (显存账本 §七) are decoded in registers; with
 // per-token K scales (ldpk §5.2) each token's score takes its own K scale.
 // Under a sliding window (ldpk §5.3) only the blocks holding the last W positions are listed,
-// so the work, the bytes and the table entries read scale with W, not with the context.
+// so the work, the bytes and the table entries read scale with W, not with the context.  With
+// anchors (pa_decode_attention_anchored) the first tokens stay visible beside the window: their
+// blocks are listed in front of the window's.
 //
 // Design (GB300, sm_103a):
 //  * Work unit = one 16-token physical block of one head group.  A CTA owns a contiguous range
@@ -74,6 +76,7 @@ constexpr float kNegInf = -INFINITY;
 struct DecodeParams {
   int B, H_q, H_kv, G, num_blocks, max_blocks, num_sink, max_ctx;
   int window;  // sliding window in tokens, 0 = whole context
+  int anchors; // positions below it stay visible beside the window (0: none)
   int hg, nc, nbs, stages, warps_c;
   int block_bytes;  // shared-memory bytes of one block in a stage
   int block_tx;     // bytes the copies of one block deliver (block_bytes less alignment padding)
@@ -114,9 +117,23 @@ __device__ __forceinline__ int seq_blocks(const DecodeParams& p, int ctx) {
   return (ctx + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE;
 }
 
-// First position the query attends: the last `window` positions (ldpk §5.3), else 0.
+// First position of the query's window: the last `window` positions (ldpk §5.3), else 0; 0 too
+// when the anchors reach the window, since everything is then attended.
 __device__ __forceinline__ int window_lo(const DecodeParams& p, int ctx) {
-  return (p.window > 0 && ctx > p.window) ? ctx - p.window : 0;
+  const int lo = (p.window > 0 && ctx > p.window) ? ctx - p.window : 0;
+  return lo <= p.anchors ? 0 : lo;
+}
+
+// Anchors of a sequence whose window starts at lo > 0 are positions [0, p.anchors); those below
+// num_sink are in the sink buffers (the merge adds them), the others in the blocks
+// [num_sink / 16, ceil(anchors / 16)), which are listed before the window's blocks.  A block that
+// holds the last anchors and the window's first positions is listed twice, once for either part:
+// the stage metadata (first, one past the last attended token) then needs no mask with a hole, and
+// the second load is an L2 hit.
+__device__ __forceinline__ int anchor_blocks(const DecodeParams& p, int lo) {
+  return (lo > 0 && p.anchors > p.num_sink)
+             ? (p.anchors + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE - p.num_sink / PA_BLOCK_SIZE
+             : 0;
 }
 
 // First position this kernel attends for sequence s (global index): the window's, or past the
@@ -129,11 +146,19 @@ __device__ __forceinline__ int seq_lo(const DecodeParams& p, int s, int ctx) {
   return shares_prefix(p, s) ? max(lo, min(p.shared_len, max(ctx, 0))) : lo;
 }
 
-// Logical blocks a sequence's query visits (those holding positions seq_lo .. ctx-1); -1 for an
-// invalid context.
+// First logical block of a sequence's window part.  With anchors, blocks that hold sink positions only
+// are left out: they may have been released (their rows come from the sink buffers).
+__device__ __forceinline__ int window_block(const DecodeParams& p, int lo) {
+  return (p.anchors > 0 ? max(lo, p.num_sink) : lo) / PA_BLOCK_SIZE;
+}
+
+// Logical blocks a sequence's query visits (those holding positions seq_lo .. ctx-1, and its
+// anchors'); -1 for an invalid context.
 __device__ __forceinline__ int seq_span(const DecodeParams& p, int s, int ctx) {
   const int nb = seq_blocks(p, ctx);
-  return nb <= 0 ? nb : nb - seq_lo(p, s, ctx) / PA_BLOCK_SIZE;
+  if (nb <= 0) return nb;
+  const int lo = seq_lo(p, s, ctx);
+  return nb - min(nb, window_block(p, lo)) + anchor_blocks(p, lo);
 }
 
 // Largest s in [0, n) with cum[s] <= u (cum non-decreasing, cum[0] <= u).
@@ -695,9 +720,14 @@ struct Producer {
   unsigned live_mask, wait_mask;
   bool waited;
 
-  // logical block of list entry u of sequence s (the visited blocks start at the window)
+  // whether list entry u of sequence s is one of its anchors' blocks
+  static __device__ __forceinline__ bool is_anchor(const DecodeParams& p, const Smem& sm, int s, int u) {
+    return u - sm.cum[s] < anchor_blocks(p, sm.los[s]);
+  }
+  // logical block of list entry u of sequence s (the anchors' blocks, then the window's)
   static __device__ __forceinline__ int logical(const DecodeParams& p, const Smem& sm, int s, int u) {
-    return sm.los[s] / PA_BLOCK_SIZE + (u - sm.cum[s]);
+    const int i = u - sm.cum[s], na = anchor_blocks(p, sm.los[s]);
+    return i < na ? p.num_sink / PA_BLOCK_SIZE + i : window_block(p, sm.los[s]) + i - na;
   }
   static __device__ __forceinline__ int load_entry(const DecodeParams& p, const Smem& sm, const Range& r, int u) {
     if (u >= r.u1) return -1;
@@ -720,10 +750,13 @@ struct Producer {
     const int lb = valid ? logical(p, sm, s, u) : 0;
     const bool bad = valid && (cur_pb < 0 || cur_pb >= p.num_blocks);
     if (bad) set_error(p.err, PA_EFLAG_BAD_BLOCK_ID);
-    // first attended token of the block: sinks and positions before the window are skipped
-    const int first =
-        valid ? min(PA_BLOCK_SIZE, max(0, max(p.num_sink, sm.los[s]) - lb * PA_BLOCK_SIZE)) : 0;
-    my_meta = valid ? make_int4(s, first, min(PA_BLOCK_SIZE, sm.ctxs[s] - lb * PA_BLOCK_SIZE), bad ? 1 : 0)
+    // attended tokens of the block: sinks and positions before the window are skipped, and of an
+    // anchors' block only the anchors are taken
+    const bool anchor = valid && is_anchor(p, sm, s, u);
+    const int from = valid && !anchor ? max(p.num_sink, sm.los[s]) : p.num_sink;
+    const int to = anchor ? p.anchors : (valid ? sm.ctxs[s] : 0);
+    const int first = valid ? min(PA_BLOCK_SIZE, max(0, from - lb * PA_BLOCK_SIZE)) : 0;
+    my_meta = valid ? make_int4(s, first, min(PA_BLOCK_SIZE, to - lb * PA_BLOCK_SIZE), bad ? 1 : 0)
                     : make_int4(-1, 0, 0, 1);
     live_mask = __ballot_sync(0xffffffffu, valid && !bad);
     // blocks that receive this step's appended token (the append's position of the sequence)
@@ -1028,13 +1061,13 @@ __global__ void __launch_bounds__(128) merge_kernel(const DecodeParams p, int gr
   }
   const int ctx = p.context_lens[s];
   const int nb = seq_span(p, s, ctx);
-  // sink positions inside the attended range [seq_lo, ctx)
-  const int sink_lo = seq_lo(p, s, ctx);
+  // sink positions inside the attended range [seq_lo, ctx), and those below sink_a (anchors)
+  const int sink_lo = seq_lo(p, s, ctx), sink_a = min(p.anchors, sink_lo);
   // partial rows of a shared prefix attended apart (only when this sequence has one)
   const int n_x = (nb < 0 || !shares_prefix(p, s)) ? 0 : p.n_extra;
   const int n_sink = (nb < 0 || part != 0) ? 0 : min(p.num_sink, ctx);
   float qv[E];
-  if (n_sink > sink_lo) {
+  if (n_sink > sink_lo || (n_sink > 0 && sink_a > 0)) {
     const __nv_bfloat16* qrow = p.q + (static_cast<size_t>(s) * p.H_q + h) * D + lane * E;
 #pragma unroll
     for (int e = 0; e < E; ++e) qv[e] = __bfloat162float(qrow[e]);
@@ -1121,7 +1154,8 @@ __global__ void __launch_bounds__(128) merge_kernel(const DecodeParams p, int gr
   }
   bad = __any_sync(0xffffffffu, bad);
 
-  for (int t = sink_lo; t < n_sink; ++t) {  // bf16 sink tokens join the merge as single-token partials
+  // bf16 sink tokens join the merge as single-token partials: the anchors among them, then the window's
+  for (int t = sink_a > 0 ? 0 : sink_lo; t < n_sink; t = t + 1 == sink_a ? sink_lo : t + 1) {
     const size_t off = ((static_cast<size_t>(s) * p.num_sink + t) * p.H_kv + h_kv) * D + lane * E;
     float dot = 0.f;
 #pragma unroll
@@ -1182,7 +1216,7 @@ struct Plan {
 };
 
 
-pa_status make_plan(const pa_cache_desc* d, int max_ctx, int partition_size, Plan* pl) {
+pa_status make_plan(const pa_cache_desc* d, int max_ctx, int partition_size, Plan* pl, int anchors = 0) {
   pa_status st = validate_desc(d);
   if (st != PA_OK) return st;
   if (max_ctx < 0 || partition_size < 0 || partition_size % PA_BLOCK_SIZE != 0) return PA_ERR_INVALID_ARG;
@@ -1231,8 +1265,14 @@ pa_status make_plan(const pa_cache_desc* d, int max_ctx, int partition_size, Pla
     pl->mode = 1;
     pl->ppb = part / PA_BLOCK_SIZE;
     int max_blk = (max_ctx + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE;
-    // a window of W positions spans at most ceil((W-1)/16) + 1 blocks
-    if (d->sliding_window > 0) max_blk = std::min(max_blk, (d->sliding_window + 14) / PA_BLOCK_SIZE + 1);
+    // a window of W positions spans at most ceil((W-1)/16) + 1 blocks, the anchors ceil(A/16) more
+    // (one of which the window's first block may be)
+    if (d->sliding_window > 0) {
+      const long long span = static_cast<long long>(d->sliding_window) / PA_BLOCK_SIZE + 2 +
+                             (static_cast<long long>(anchors) + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE;
+      if (anchors > 0) max_blk = static_cast<int>(std::min<long long>(max_blk + 1LL, span));
+      else max_blk = std::min(max_blk, (d->sliding_window + 14) / PA_BLOCK_SIZE + 1);
+    }
     pl->max_parts = std::max(1, (max_blk + pl->ppb - 1) / pl->ppb);
     pl->grid_x = pl->max_parts;
     pl->n_slots = static_cast<size_t>(B) * pl->max_parts;
@@ -1296,15 +1336,15 @@ struct SharedPart {
   int n_extra;
 };
 
-// pa_decode_attention, the attention half of pa_decode_step (append_pos non-null) and the
-// decode half of pa_decode_attention_shared (shared non-null).
+// pa_decode_attention, the attention half of pa_decode_step (append_pos non-null), the decode half
+// of pa_decode_attention_shared (shared non-null) and pa_decode_attention_anchored (anchors > 0).
 pa_status decode_attention_impl(const pa_cache_desc* desc, void* out, const void* q, const void* k_cache,
                                 const void* v_cache, const int32_t* block_tables, const int32_t* context_lens,
                                 int max_context_len, float scale, int partition_size, void* workspace,
                                 size_t workspace_bytes, int32_t* err_flag, void* stream, const int32_t* append_pos,
-                                const SharedPart* shared = nullptr) {
+                                const SharedPart* shared = nullptr, int anchors = 0) {
   pa::Plan pl;
-  pa_status st = pa::make_plan(desc, max_context_len, partition_size, &pl);
+  pa_status st = pa::make_plan(desc, max_context_len, partition_size, &pl, anchors);
   if (st != PA_OK) return st;
   if (desc->num_seqs == 0) return PA_OK;
   if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !workspace)
@@ -1349,6 +1389,7 @@ pa_status decode_attention_impl(const pa_cache_desc* desc, void* out, const void
   p.max_blocks = desc->max_blocks_per_seq;
   p.num_sink = desc->num_sink;
   p.window = desc->sliding_window;
+  p.anchors = desc->sliding_window > 0 ? std::min(std::min(anchors, max_context_len), 0x7FFFFF00) : 0;
   p.max_ctx = max_context_len;
   p.hg = pl.hg;
   p.nc = pl.nc;
@@ -1425,6 +1466,25 @@ extern "C" pa_status pa_decode_step(const pa_cache_desc* desc, void* out, const 
   if (st != PA_OK) return st;
   return pa::decode_attention_impl(desc, out, q, k_cache, v_cache, block_tables, context_lens, max_context_len,
                                    scale, partition_size, workspace, workspace_bytes, err_flag, stream, positions);
+}
+
+extern "C" size_t pa_decode_anchored_workspace_size(const pa_cache_desc* desc, int max_context_len,
+                                                    int partition_size, int num_anchor) {
+  pa::Plan pl;
+  if (num_anchor < 0 || pa::make_plan(desc, max_context_len, partition_size, &pl, num_anchor) != PA_OK) return 0;
+  return pl.ws_bytes;
+}
+
+extern "C" pa_status pa_decode_attention_anchored(const pa_cache_desc* desc, void* out, const void* q,
+                                                  const void* k_cache, const void* v_cache,
+                                                  const int32_t* block_tables, const int32_t* context_lens,
+                                                  int max_context_len, float scale, int partition_size,
+                                                  int num_anchor, void* workspace, size_t workspace_bytes,
+                                                  int32_t* err_flag, void* stream) {
+  if (num_anchor < 0) return PA_ERR_INVALID_ARG;
+  return pa::decode_attention_impl(desc, out, q, k_cache, v_cache, block_tables, context_lens, max_context_len,
+                                   scale, partition_size, workspace, workspace_bytes, err_flag, stream, nullptr,
+                                   nullptr, num_anchor);
 }
 
 // ------------------------------------------------------------------------------------

@@ -8,6 +8,9 @@
 // §四), with GQA grouping (same page §二).  Under a sliding window of W tokens (ldpk §5.3) the
 // query at position p reads keys p-W+1 .. p only, and blocks before a tile's window are not read.
 //
+// With anchors (pa_prefill_attention_anchored) positions below A stay visible beside the window: a
+// tile's blocks are the anchors' and then its window's (one run of blocks when the two meet).
+//
 // Design: one CTA per (sequence, KV head, tile of query tokens).  Four consumer warps own 16
 // (query token, query head) rows each, so every K/V element a warp loads serves up to 16 query
 // rows; S = Q·Kᵀ and O += P·V are m16n8k16 tensor-core products with the queries as M, and P is
@@ -41,6 +44,7 @@ constexpr float kNegInfP = -INFINITY;
 struct PrefillParams {
   int B, H_q, H_kv, G, num_blocks, max_blocks, max_q;
   int window;  // sliding window in tokens, 0 = whole context
+  int anchors; // positions below it stay visible beside the window (0: none)
   int tpw;     // query tokens per warp (16 / G)
   int q_tile;  // query tokens per CTA
   int nc;      // 128-byte chunks per head row
@@ -62,6 +66,35 @@ struct PrefillParams {
   const __nv_bfloat16* v_sink;
   size_t extra_offset;
 };
+
+// The blocks a query tile reads: [0, ab), then [kb0, kb0 + n - ab); ab = 0 without anchors, and
+// when the anchors' blocks reach kb0 (the list is then one run from block 0).  kv_lo: first key of
+// the window part (0 when the anchors reach it); kv_end: one past the last key.
+struct BlockList {
+  int ab, kb0, n, lo;
+  __device__ __forceinline__ BlockList(const PrefillParams& p, int kv_lo, int kv_end) : lo(kv_lo) {
+    kb0 = kv_lo / PA_BLOCK_SIZE;
+    ab = p.window > 0 ? (p.anchors + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE : 0;
+    if (ab >= kb0) {
+      if (ab > 0) kb0 = 0;
+      ab = 0;
+    }
+    n = ab + (kv_end + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE - kb0;
+  }
+  __device__ __forceinline__ int block(int k) const { return k < ab ? k : kb0 + k - ab; }
+  // Whether logical block b holds an attended position outside the sink buffers; the table entry of
+  // another block is not looked at (it may have been released).
+  __device__ __forceinline__ bool paged(const PrefillParams& p, int b) const {
+    const int first = max(p.num_sink, b * PA_BLOCK_SIZE), end = (b + 1) * PA_BLOCK_SIZE;
+    return end > max(first, lo) || min(p.anchors, end) > first;
+  }
+};
+
+// First key of the window of the query at position pos; 0 when the anchors reach it.
+__device__ __forceinline__ int key_lo(const PrefillParams& p, int pos) {
+  const int lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+  return lo <= p.anchors ? 0 : lo;
+}
 
 // One consumer warp's 16 query rows of a prefill tile: row r = (token r / G, query head r % G) of
 // the warp's tpw = 16 / G query tokens.  S = Q·Kᵀ and O += P·V are m16n8k16 tensor-core products
@@ -89,7 +122,7 @@ struct PrefillRows {
     w_tokens = max(0, min(p.tpw, t_end - wt0));
     w_last_pos = first_pos + wt0 + w_tokens - 1;  // last query position of this warp
     // lowest key any row of this warp reads (its first token's window start)
-    w_lo = p.window > 0 ? max(0, first_pos + wt0 - p.window + 1) : 0;
+    w_lo = key_lo(p, first_pos + wt0);
     // rows past the tokens are padding
     const int rows_used = w_tokens * p.G;
 #pragma unroll
@@ -120,7 +153,8 @@ struct PrefillRows {
   // One block of 16 keys at positions kbase_pos.. (kv_end: first key past the tile's queries).
   __device__ __forceinline__ void block(const PrefillParams& p, const uint8_t* kt, const uint8_t* vt, int kbase_pos,
                                         int kv_end) {
-    if (!(w_tokens > 0 && kbase_pos <= w_last_pos && kbase_pos + PA_BLOCK_SIZE > w_lo)) return;
+    if (!(w_tokens > 0 && kbase_pos <= w_last_pos && (kbase_pos + PA_BLOCK_SIZE > w_lo || kbase_pos < p.anchors)))
+      return;
     // S = Q Kᵀ for the 16 keys (two n-tiles of 8)
     float sacc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
     {
@@ -146,7 +180,8 @@ struct PrefillRows {
 #pragma unroll
         for (int jj = 0; jj < 2; ++jj) {
           const int kp = kbase_pos + nt * 8 + 2 * tq + jj;
-          const bool ok = row_ok[half] && kp <= row_pos[half] && (p.window <= 0 || kp > row_pos[half] - p.window);
+          const bool ok = row_ok[half] && kp <= row_pos[half] &&
+                          (p.window <= 0 || kp > row_pos[half] - p.window || kp < p.anchors);
           const float v = ok ? sacc[nt][2 * half + jj] * p.scale_log2 : kNegInfP;
           sv[half][nt][jj] = v;
           bm[half] = fmaxf(bm[half], v);
@@ -197,8 +232,8 @@ struct PrefillRows {
     // (b0, b2) and 8+2tq, 9+2tq (b1, b3).
     uint32_t vlo = 0xFFFFFFFFu, vhi = 0xFFFFFFFFu;
     if (kbase_pos + PA_BLOCK_SIZE > kv_end || kbase_pos < w_lo) {
-      const int hi = kv_end - kbase_pos, lo = w_lo - kbase_pos;
-      auto keep = [&](int r) { return r < hi && r >= lo; };
+      const int hi = kv_end - kbase_pos, lo = w_lo - kbase_pos, an = p.anchors - kbase_pos;
+      auto keep = [&](int r) { return r < hi && (r >= lo || r < an); };
       vlo = (keep(2 * tq) ? 0x0000FFFFu : 0u) | (keep(2 * tq + 1) ? 0xFFFF0000u : 0u);
       vhi = (keep(2 * tq + 8) ? 0x0000FFFFu : 0u) | (keep(2 * tq + 9) ? 0xFFFF0000u : 0u);
     }
@@ -271,9 +306,8 @@ __global__ void __launch_bounds__(kPfThreads)
   const int first_pos = ctx - n;
   const int t_end = min(n, t0 + p.q_tile);
   const int kv_end = first_pos + t_end;  // keys [kv_lo, kv_end) are visible to this tile
-  const int kv_lo = p.window > 0 ? max(0, first_pos + t0 - p.window + 1) : 0;
-  const int kb0 = kv_lo / PA_BLOCK_SIZE;  // first logical block read
-  const int n_blocks = (kv_end + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE - kb0;
+  const BlockList bl(p, key_lo(p, first_pos + t0), kv_end);  // the logical blocks read
+  const int n_blocks = bl.n;
 
   if (tid == 0) {
     for (int i = 0; i < kPfStages; ++i) {
@@ -287,14 +321,15 @@ __global__ void __launch_bounds__(kPfThreads)
   if (warp == kPfWarps) {
     // ------------------------------ producer ------------------------------
     const uint64_t policy = l2_evict_first_policy();
-    const int32_t* row = p.block_tables + static_cast<size_t>(s) * p.max_blocks + kb0;
-    int cur = lane < n_blocks ? row[lane] : -1;
-    int nxt = 32 + lane < n_blocks ? row[32 + lane] : -1;
+    const int32_t* row = p.block_tables + static_cast<size_t>(s) * p.max_blocks;
+    auto entry = [&](int k) { return k < n_blocks ? row[bl.block(k)] : -1; };
+    int cur = entry(lane);
+    int nxt = entry(32 + lane);
     int k = 0;
     for (; k < n_blocks; ++k) {
       if (k > 0 && (k & 31) == 0) {
         cur = nxt;
-        nxt = k + 32 + lane < n_blocks ? row[k + 32 + lane] : -1;
+        nxt = entry(k + 32 + lane);
       }
       const int pb = __shfl_sync(0xffffffffu, cur, k & 31);
       const bool bad = pb < 0 || pb >= p.num_blocks;
@@ -339,7 +374,7 @@ __global__ void __launch_bounds__(kPfThreads)
       return;
     }
     if (bad_stage[st]) w.bad = true;
-    else w.block(p, stages[st], stages[st] + NC * kChunkTile, (kb0 + k) * PA_BLOCK_SIZE, kv_end);
+    else w.block(p, stages[st], stages[st] + NC * kChunkTile, bl.block(k) * PA_BLOCK_SIZE, kv_end);
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[st]);
   }
@@ -490,10 +525,9 @@ __global__ void __launch_bounds__(kPfWarps * 32)
   const int first_pos = ctx - n;
   const int t_end = min(n, t0 + p.q_tile);
   const int kv_end = first_pos + t_end;
-  const int kv_lo = p.window > 0 ? max(0, first_pos + t0 - p.window + 1) : 0;
-  const int kb0 = kv_lo / PA_BLOCK_SIZE;
-  const int n_blocks = (kv_end + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE - kb0;
-  const int32_t* trow = p.block_tables + static_cast<size_t>(s) * p.max_blocks + kb0;
+  const BlockList bl(p, key_lo(p, first_pos + t0), kv_end);
+  const int n_blocks = bl.n;
+  const int32_t* trow = p.block_tables + static_cast<size_t>(s) * p.max_blocks;
 
   PrefillRows<D> w;
   w.init(p, warp, lane, qs, h_kv, t0, t_end, first_pos);
@@ -502,16 +536,16 @@ __global__ void __launch_bounds__(kPfWarps * 32)
   const bool piece = tid < PIECES;
   const int pt = tid / (16 * GROUPS), pr = (tid / GROUPS) % 16, pg = tid % GROUPS;
   DqPiece<D, KIND> cur;
-  // Block k's table entry, or -1 when the block holds only sink positions (its slots are never
+  // Block k's table entry, or -1 when only sink positions of it are attended (its slots are never
   // read) and -2 when the entry is outside the pool.
   auto entry = [&](int k) -> int {
-    const int kpos = (kb0 + k) * PA_BLOCK_SIZE;
-    if (kpos + PA_BLOCK_SIZE <= p.num_sink) return -1;
-    const int e = trow[k];
+    const int kb = bl.block(k);
+    if (!bl.paged(p, kb)) return -1;
+    const int e = trow[kb];
     return (e < 0 || e >= p.num_blocks) ? -2 : e;
   };
   auto load = [&](int k, int e) {
-    const int pos = (kb0 + k) * PA_BLOCK_SIZE + pr;
+    const int pos = bl.block(k) * PA_BLOCK_SIZE + pr;
     if (piece && e != -2 && (e >= 0 || pos < p.num_sink))
       cur.load(p, pt, s, h_kv, pos, static_cast<size_t>(max(e, 0)) * PA_BLOCK_SIZE + pr, pg);
   };
@@ -531,7 +565,7 @@ __global__ void __launch_bounds__(kPfWarps * 32)
     }
     __syncthreads();
     if (bad_blk[k & 1]) w.bad = true;
-    else w.block(p, wk, wk + TILE, (kb0 + k) * PA_BLOCK_SIZE, kv_end);
+    else w.block(p, wk, wk + TILE, bl.block(k) * PA_BLOCK_SIZE, kv_end);
   }
   w.finish(p, qs, h_kv);
 }
@@ -543,30 +577,43 @@ __global__ void __launch_bounds__(kPfWarps * 32)
 // prefill_dq_kernel: code times scale in fp32 rounded to bf16, sink positions from the sink
 // buffers), and writes the dense table entry dense[s][b]: that block, or -1 for a block no query
 // attends or whose table entry lies outside the pool (the attention kernel then reports it).
+// With cap > 0 (pa_prefill_attention_anchored) the pool holds only the cap blocks per sequence that
+// the chunk's queries can attend: CTA (i, s) takes the i-th of them, the anchors' blocks and then the
+// window's, into block s * cap + i, and dense[s][b] of that logical block b names it; the entries of
+// other blocks are not written (nor read).
 // ------------------------------------------------------------------------------------
 template <int D, int KIND>
 __global__ void __launch_bounds__(256)
-    prefill_expand_kernel(const PrefillParams p, int mb, __nv_bfloat16* kx, __nv_bfloat16* vx, int32_t* dense) {
+    prefill_expand_kernel(const PrefillParams p, int mb, __nv_bfloat16* kx, __nv_bfloat16* vx, int32_t* dense,
+                          int cap) {
   constexpr int GROUPS = D / 32;
-  const int b = blockIdx.x, s = blockIdx.y;
+  const int s = blockIdx.y;
+  int b = blockIdx.x;
   grid_dep_wait();  // the previous kernel of the stream may still be writing any input
   const int n = p.q_start[s + 1] - p.q_start[s];
   const int ctx = p.context_lens[s];
   const bool valid = n >= 0 && n <= ctx && n <= p.max_q && ctx <= p.max_blocks * PA_BLOCK_SIZE &&
                      ctx <= mb * PA_BLOCK_SIZE;
   // the positions the chunk's queries attend: from the first query's window start to ctx - 1
-  const int lo = p.window > 0 ? max(0, ctx - n - p.window + 1) : 0;
+  const int lo = key_lo(p, ctx - n);
+  int first = lo / PA_BLOCK_SIZE;  // first block to decode
+  const BlockList bl(p, lo, ctx);
+  if (cap > 0) {
+    b = bl.block(b);
+    first = 0;
+  }
   int e = -1;  // the block's pool entry (0 for a block of sink positions only: none is read)
-  if (valid && b >= lo / PA_BLOCK_SIZE && b * PA_BLOCK_SIZE < ctx) {
-    if ((b + 1) * PA_BLOCK_SIZE <= p.num_sink) {
+  if (valid && b >= first && b < mb && b * PA_BLOCK_SIZE < ctx) {
+    if (!bl.paged(p, b)) {
       e = 0;
     } else {
       const int t = p.block_tables[static_cast<size_t>(s) * p.max_blocks + b];
       e = (t < 0 || t >= p.num_blocks) ? -1 : t;
     }
   }
-  const size_t xb = static_cast<size_t>(s) * mb + b;  // the block of the bf16 pool
-  if (threadIdx.x == 0) dense[xb] = e >= 0 ? static_cast<int32_t>(xb) : -1;
+  // the block of the bf16 pool
+  const size_t xb = static_cast<size_t>(s) * (cap > 0 ? cap : mb) + blockIdx.x;
+  if (threadIdx.x == 0 && b < mb) dense[static_cast<size_t>(s) * mb + b] = e >= 0 ? static_cast<int32_t>(xb) : -1;
   if (e < 0) return;
   const int pieces = 2 * PA_BLOCK_SIZE * p.H_kv * GROUPS;  // (tensor, slot, head, 32-dim group)
   for (int i = threadIdx.x; i < pieces; i += blockDim.x) {
@@ -608,7 +655,8 @@ pa_status prefill_check(const pa_cache_desc* desc, const void* out, const void* 
 
 PrefillParams prefill_params(const pa_cache_desc* desc, void* out, const void* q, const void* k_cache,
                              const void* v_cache, const int32_t* block_tables, const int32_t* q_start,
-                             const int32_t* context_lens, int max_query_len, float scale, int32_t* err_flag) {
+                             const int32_t* context_lens, int max_query_len, float scale, int32_t* err_flag,
+                             int anchors) {
   PrefillParams p;
   p.B = desc->num_seqs;
   p.H_q = desc->num_q_heads;
@@ -618,6 +666,7 @@ PrefillParams prefill_params(const pa_cache_desc* desc, void* out, const void* q
   p.max_blocks = desc->max_blocks_per_seq;
   p.max_q = max_query_len;
   p.window = desc->sliding_window;
+  p.anchors = p.window > 0 ? anchors : 0;
   p.tpw = 16 / p.G;
   p.q_tile = kPfWarps * p.tpw;
   p.nc = desc->head_dim * 2 / 128;
@@ -643,14 +692,14 @@ PrefillParams prefill_params(const pa_cache_desc* desc, void* out, const void* q
 pa_status prefill_launch(const pa_cache_desc* desc, void* out, const void* q, const void* k_cache,
                          const void* v_cache, const int32_t* block_tables, const int32_t* q_start,
                          const int32_t* context_lens, int max_query_len, float scale, int32_t* err_flag,
-                         void* stream, bool step) {
+                         void* stream, bool step, int anchors = 0) {
   const int D = desc->head_dim;
   const int G = desc->num_q_heads / desc->num_kv_heads;
   const bool dq = is_quantized(desc) || desc->num_sink > 0;  // decoded per block (prefill_dq_kernel)
 #ifndef PA_PREFILL_WARP_MMA_ONLY
   if (!dq && D == 128 && (G & (G - 1)) == 0)  // the tensor-core (tcgen05) kernel
     return launch_prefill_tc(desc, out, q, k_cache, v_cache, block_tables, q_start, context_lens, max_query_len,
-                             scale, err_flag, as_stream(stream), step);
+                             scale, err_flag, as_stream(stream), step, anchors);
 #endif
   (void)step;  // the warp-MMA kernel waits for its predecessor before it starts
   const int nc = D * 2 / 128;
@@ -660,7 +709,7 @@ pa_status prefill_launch(const pa_cache_desc* desc, void* out, const void* q, co
               !encode_cache_map(&mv, v_cache, 2, desc->num_kv_heads * nc, 1, slots)))
     return PA_ERR_CUDA;
   const PrefillParams p = prefill_params(desc, out, q, k_cache, v_cache, block_tables, q_start, context_lens,
-                                         max_query_len, scale, err_flag);
+                                         max_query_len, scale, err_flag, anchors);
   const dim3 grid((max_query_len + p.q_tile - 1) / p.q_tile, p.B, p.H_kv);
   cudaStream_t s = as_stream(stream);
   if (dq) {  // 8-bit and INT4 caches have head_dim 128 (validate_desc)
@@ -699,38 +748,56 @@ size_t prefill_ws_bytes(const pa_cache_desc* d, int max_ctx, int* mb_out) {
 #endif
 }
 
+// The same for pa_prefill_attention_anchored, whose pool holds *cap blocks per sequence: the anchors'
+// blocks and those of the positions that a chunk of max_q queries can attend through its window.
+size_t prefill_anchored_ws_bytes(const pa_cache_desc* d, int max_q, int max_ctx, int anchors, int* mb_out,
+                                 int* cap_out) {
+  int mb = 0;
+  if (max_q < 0 || anchors < 0 || prefill_ws_bytes(d, max_ctx, &mb) == 0) return 0;
+  long long cap = mb;
+  if (d->sliding_window > 0)
+    cap = std::min(cap, (static_cast<long long>(std::min(anchors, max_ctx)) + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE +
+                            (static_cast<long long>(d->sliding_window) + max_q) / PA_BLOCK_SIZE + 2);
+  *mb_out = mb;
+  *cap_out = static_cast<int>(cap);
+  const size_t table = (static_cast<size_t>(d->num_seqs) * mb * 4 + 255) / 256 * 256;
+  return table + 2 * (static_cast<size_t>(d->num_seqs) * cap * PA_BLOCK_SIZE * d->num_kv_heads * 128 * 2);
+}
+
 // The expanded path: decode every attended block once into the workspace's bf16 pool, then the
-// tensor-core kernel over that pool and its dense table (as a bf16 cache without sinks).
+// tensor-core kernel over that pool and its dense table (as a bf16 cache without sinks).  cap > 0: the
+// pool's blocks per sequence (see prefill_expand_kernel), else mb.
 pa_status prefill_expanded(const pa_cache_desc* desc, void* out, const void* q, const void* k_cache,
                            const void* v_cache, const int32_t* block_tables, const int32_t* q_start,
                            const int32_t* context_lens, int max_query_len, float scale, int mb, void* workspace,
-                           int32_t* err_flag, void* stream) {
+                           int32_t* err_flag, void* stream, int cap = 0, int anchors = 0) {
   const PrefillParams p = prefill_params(desc, out, q, k_cache, v_cache, block_tables, q_start, context_lens,
-                                         max_query_len, scale, err_flag);
+                                         max_query_len, scale, err_flag, anchors);
+  const int per_seq = cap > 0 ? cap : mb;
   const size_t table = (static_cast<size_t>(desc->num_seqs) * mb * 4 + 255) / 256 * 256;
-  const size_t pool = static_cast<size_t>(desc->num_seqs) * mb * PA_BLOCK_SIZE * desc->num_kv_heads * 128 * 2;
+  const size_t pool = static_cast<size_t>(desc->num_seqs) * per_seq * PA_BLOCK_SIZE * desc->num_kv_heads * 128 * 2;
   int32_t* dense = static_cast<int32_t*>(workspace);
   auto* kx = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(workspace) + table);
   auto* vx = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(workspace) + table + pool);
   cudaStream_t s = as_stream(stream);
-  const dim3 grid(mb, desc->num_seqs), block(256);
+  const dim3 grid(per_seq, desc->num_seqs), block(256);
   pa_status st;
-  if (is_int4(desc)) st = launch_overlapped(prefill_expand_kernel<128, 2>, grid, block, 0, s, p, mb, kx, vx, dense);
+  if (is_int4(desc)) st = launch_overlapped(prefill_expand_kernel<128, 2>, grid, block, 0, s, p, mb, kx, vx, dense, cap);
   else if (has_token_scales(desc))
-    st = launch_overlapped(prefill_expand_kernel<128, 3>, grid, block, 0, s, p, mb, kx, vx, dense);
+    st = launch_overlapped(prefill_expand_kernel<128, 3>, grid, block, 0, s, p, mb, kx, vx, dense, cap);
   else if (is_quantized(desc))
-    st = launch_overlapped(prefill_expand_kernel<128, 1>, grid, block, 0, s, p, mb, kx, vx, dense);
-  else st = launch_overlapped(prefill_expand_kernel<128, 0>, grid, block, 0, s, p, mb, kx, vx, dense);
+    st = launch_overlapped(prefill_expand_kernel<128, 1>, grid, block, 0, s, p, mb, kx, vx, dense, cap);
+  else st = launch_overlapped(prefill_expand_kernel<128, 0>, grid, block, 0, s, p, mb, kx, vx, dense, cap);
   if (st != PA_OK) return st;
   pa_cache_desc x = *desc;  // the bf16 pool: every attended block, sinks included, in place
   x.k_dtype = x.v_dtype = PA_BF16;
   x.k_scales = x.v_scales = nullptr;
   x.k_sink = x.v_sink = nullptr;
   x.num_sink = 0;
-  x.num_blocks = desc->num_seqs * mb;
+  x.num_blocks = desc->num_seqs * per_seq;
   x.max_blocks_per_seq = mb;
   return launch_prefill_tc(&x, out, q, kx, vx, dense, q_start, context_lens, max_query_len, scale, err_flag, s,
-                           false);
+                           false, anchors);
 }
 }  // namespace
 }  // namespace pa
@@ -764,6 +831,43 @@ extern "C" pa_status pa_prefill_attention_ws(const pa_cache_desc* desc, void* ou
                               scale, err_flag, stream, false);
   return pa::prefill_expanded(desc, out, q, k_cache, v_cache, block_tables, q_start, context_lens, max_query_len,
                               scale, mb, workspace, err_flag, stream);
+}
+
+extern "C" size_t pa_prefill_anchored_workspace_size(const pa_cache_desc* desc, int max_query_len,
+                                                     int max_context_len, int num_anchor) {
+  int mb = 0, cap = 0;
+  return pa::prefill_anchored_ws_bytes(desc, max_query_len, max_context_len, num_anchor, &mb, &cap);
+}
+
+extern "C" pa_status pa_prefill_attention_anchored(const pa_cache_desc* desc, void* out, const void* q,
+                                                   const void* k_cache, const void* v_cache,
+                                                   const int32_t* block_tables, const int32_t* q_start,
+                                                   const int32_t* context_lens, int max_query_len,
+                                                   int max_context_len, float scale, int num_anchor,
+                                                   void* workspace, size_t workspace_bytes, int32_t* err_flag,
+                                                   void* stream) {
+  bool work = false;
+  const pa_status st = pa::prefill_check(desc, out, q, k_cache, v_cache, block_tables, q_start, context_lens,
+                                         max_query_len, scale, &work);
+  if (st != PA_OK) return st;
+  if (num_anchor < 0 || !(scale > 0.f) || max_context_len < 0 ||
+      static_cast<long long>(max_context_len) > static_cast<long long>(desc->max_blocks_per_seq) * PA_BLOCK_SIZE)
+    return PA_ERR_INVALID_ARG;
+  int mb = 0, cap = 0;
+  const size_t need = pa::prefill_anchored_ws_bytes(desc, max_query_len, max_context_len, num_anchor, &mb, &cap);
+  if (need > 0) {
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return PA_ERR_INVALID_ARG;
+    if (workspace_bytes < need) return PA_ERR_WORKSPACE_TOO_SMALL;
+  }
+  if (!work) return PA_OK;
+  // no position lies past the table, and anchors + 15 must stay within an int
+  const int anchors = static_cast<int>(std::min<long long>(
+      num_anchor, std::min(static_cast<long long>(desc->max_blocks_per_seq) * PA_BLOCK_SIZE, 0x7FFFFF00LL)));
+  if (need == 0)
+    return pa::prefill_launch(desc, out, q, k_cache, v_cache, block_tables, q_start, context_lens, max_query_len,
+                              scale, err_flag, stream, false, anchors);
+  return pa::prefill_expanded(desc, out, q, k_cache, v_cache, block_tables, q_start, context_lens, max_query_len,
+                              scale, mb, workspace, err_flag, stream, cap, anchors);
 }
 
 extern "C" pa_status pa_prefill_step_ws(const pa_cache_desc* desc, void* out, const void* q, void* k_cache,

@@ -46,6 +46,12 @@
 //    then: its P·V was issued before this S).  V rows of keys that are not loaded or lie beyond
 //    the context are zeroed before P·V reads them, so bits left in unused slots (NaN included)
 //    cannot leak.
+//  * Anchors (pa_prefill_attention_anchored; ANCH, a template parameter, so that the plain kernel
+//    carries none of it): the first A positions stay visible beside the window.  An item lists the
+//    anchors' blocks and then its window's as one sequence of blocks, cut into tiles of 8, so four
+//    anchors cost one block, not a tile of their own.  In a tile, key column c is an anchor iff
+//    c < A - 128k (the list starts at position 0), and the window's columns are at
+//    (kb0 - ab + 8k) 16 + c, so a row's mask is two intervals: [0, A - 128k) and [lo, hi].
 //  * Output: O / l as bf16 is staged in the idle ring stage of the item's last tile (K for query
 //    tile 0, V for query tile 1) and stored by TMA; the stage is then released to its copy warp.
 //    Only a tile holding rows past its sequence is stored row by row.
@@ -88,6 +94,7 @@ constexpr uint32_t kIdescPV = kIdescS | (1u << 16);
 
 struct TcParams {
   int B, H_q, H_kv, G, num_blocks, max_blocks, max_q, window;
+  int anchors;  // positions below it stay visible beside the window (ANCH)
   int tpq;  // tokens per query tile: 128 / G (a CTA holds two tiles)
   int step;  // the previous kernel is this step's append: only the K/V copies wait for it
   float scale_log2;
@@ -228,10 +235,13 @@ __device__ __forceinline__ int count_ge(const SeqGeo& g, int X, int lw) {
 }
 // One work item of a CTA: the query rows of tile c of sequence s (tokens [t0, t_end) with
 // t0 = c tpc, tpc = 2 tpq tokens per tile) against KV head h_kv, in two query tiles of tpq tokens;
-// the CTA reads the keys [kv_lo, kv_end), blocks [kb0, kb_end), in n_tiles tiles of 8 blocks.
+// the CTA reads the keys [kv_lo, kv_end), blocks [kb0, kb_end), in n_tiles tiles of 8 blocks.  With
+// anchors its n_list blocks are [0, ab), then [kb0, kb_end); ab = 0 when the anchors' blocks reach
+// kb0, which is then 0 (the list is one run).
 struct Item {
-  int s, h_kv, tile, qs, n, t0, t_end, first_pos, kv_lo, kb0, kb_end, n_tiles, loaded_end;
+  int s, h_kv, tile, qs, n, t0, t_end, first_pos, kv_lo, kb0, kb_end, ab, n_list, n_tiles, loaded_end;
   bool valid, has0, has1;
+  __device__ __forceinline__ int block(int b) const { return b < ab ? b : kb0 + b - ab; }  // of list entry b
 };
 // An entry of a CTA's item list (shared memory): the sequence, the tile and KV head
 // (c << 16 | h), and the sequence's first query row, query rows and context length.
@@ -248,6 +258,7 @@ __device__ __forceinline__ ItemRec item_rec(const TcParams& p, int s, int c, int
   e.pad = 0;
   return e;
 }
+template <bool ANCH>
 __device__ __forceinline__ Item make_item(const TcParams& p, const ItemRec& e) {
   Item it;
   it.s = e.s;
@@ -263,13 +274,19 @@ __device__ __forceinline__ Item make_item(const TcParams& p, const ItemRec& e) {
   it.has1 = it.valid && it.t0 + p.tpq < it.n;
   it.first_pos = ctx - it.n;
   it.t_end = min(it.n, it.t0 + tpc);
-  it.kv_lo = it.kb0 = it.kb_end = it.n_tiles = it.loaded_end = 0;
+  it.kv_lo = it.kb0 = it.kb_end = it.ab = it.n_list = it.n_tiles = it.loaded_end = 0;
   if (it.has0) {
     const int kv_end = it.first_pos + it.t_end;
     it.kv_lo = p.window > 0 ? max(0, it.first_pos + it.t0 - p.window + 1) : 0;
+    if (ANCH && it.kv_lo <= p.anchors) it.kv_lo = 0;
     it.kb0 = it.kv_lo / PA_BLOCK_SIZE;
     it.kb_end = (kv_end + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE;
-    it.n_tiles = (it.kb_end - it.kb0 + 7) / 8;
+    if constexpr (ANCH) {
+      it.ab = (p.anchors + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE;
+      if (it.ab >= it.kb0) it.ab = it.kb0 = 0;
+    }
+    it.n_list = it.ab + it.kb_end - it.kb0;
+    it.n_tiles = (it.n_list + 7) / 8;
     it.loaded_end = min(ctx, it.kb_end * PA_BLOCK_SIZE);  // keys past this hold no loaded data
   }
   return it;
@@ -280,6 +297,7 @@ __device__ __forceinline__ Item make_item(const TcParams& p, const ItemRec& e) {
 // on the same CTA.
 __device__ __forceinline__ int round_pos(int r, int NC, int cid) { return r * NC + ((r & 1) ? NC - 1 - cid : cid); }
 
+template <bool ANCH>
 __global__ void __launch_bounds__(kTcThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
@@ -420,16 +438,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       return r;
     };
     for (int ii = 0; ok && ii < n_items; ++ii) {
-      const Item it = make_item(p, list[ii]);
+      const Item it = make_item<ANCH>(p, list[ii]);
       if (it.n_tiles == 0) continue;
       const int32_t* row = p.block_tables + static_cast<size_t>(it.s) * p.max_blocks;
-      const int kb0 = it.kb0, kb_end = it.kb_end;
       // Table entries live in registers, 32 consecutive blocks per chunk and one per lane, for
       // chunks c0, c0 + 1 and c0 + 2: the accesses only move forward, so a chunk is loaded two
       // chunks before it is first needed and its latency is hidden.
-      auto entry = [&](int c) { const int kb = kb0 + 32 * c + lane; return kb < kb_end ? row[kb] : -1; };
+      auto entry = [&](int c) { const int b = 32 * c + lane; return b < it.n_list ? row[it.block(b)] : -1; };
       int c0 = 0, e0 = entry(0), e1 = entry(1), e2 = entry(2);
-      auto table = [&](int b) -> int {  // entry of block kb0 + b; b is in the same chunk on every lane
+      auto table = [&](int b) -> int {  // entry of list block b; b is in the same chunk on every lane
         const int cb = __shfl_sync(0xffffffffu, b, 0) >> 5;
         while (cb > c0 + 1) {
           e0 = e1;
@@ -441,10 +458,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         return cb == c0 ? v0 : v1;
       };
       for (int k = 0; ok && k < it.n_tiles; ++k) {
-        const int kb = kb0 + 8 * k + lane;
         const int ent = table(8 * k + min(lane, 7));
         int pb = -1;
-        if (lane < 8 && kb < kb_end) {
+        if (lane < 8 && 8 * k + lane < it.n_list) {
           pb = ent;
           if (pb < 0 || pb >= p.num_blocks) {
             if (half == 0) set_error(p.err, PA_EFLAG_BAD_BLOCK_ID);
@@ -489,7 +505,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int qi = 0;
     const int c = lane & 15;
     for (int ii = 0; ok && ii < n_items; ++ii) {
-      const Item it = make_item(p, list[ii]);
+      const Item it = make_item<ANCH>(p, list[ii]);
       if (it.n_tiles == 0) continue;
       if (!(ok = warp_wait(q_empty, (static_cast<uint32_t>(qi) & 1u) ^ 1u))) break;
       ++qi;
@@ -561,12 +577,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // stage the output of query tiles 0 and 1 when those hold rows, and their groups release
       // them after it has left; otherwise they are released here.
       int g_tot = 0;
-      for (int ii = 0; ii < n_items; ++ii) g_tot += make_item(p, list[ii]).n_tiles;
+      for (int ii = 0; ii < n_items; ++ii) g_tot += make_item<ANCH>(p, list[ii]).n_tiles;
       bool ok = true;
       int g = 0, qi = 0;
       uint32_t sp[2] = {0u, 0u};  // tiles of each query tile so far: s_full / p_full / o_done phase
       for (int ii = 0; ok && ii < n_items; ++ii) {
-        const Item it = make_item(p, list[ii]);
+        const Item it = make_item<ANCH>(p, list[ii]);
         const int nt = it.n_tiles;
         if (nt == 0) continue;
         const int groups = it.has1 ? 2 : 1;  // query tiles with rows (an item with tiles has rows)
@@ -620,9 +636,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int g = 0;        // tiles of this CTA so far (V stage and phase)
     uint32_t sp = 0;  // tiles of this query tile so far
     int g_tot = 0;    // tiles of all the CTA's items (whether a later copy waits for a stage)
-    for (int ii = 0; ii < n_items; ++ii) g_tot += make_item(p, list[ii]).n_tiles;
+    for (int ii = 0; ii < n_items; ++ii) g_tot += make_item<ANCH>(p, list[ii]).n_tiles;
     for (int ii = 0; ii < n_items; ++ii) {
-      const Item it = make_item(p, list[ii]);
+      const Item it = make_item<ANCH>(p, list[ii]);
       const int tq0 = it.t0 + wg * p.tpq;  // first token of this query tile
       uint4* orow = reinterpret_cast<uint4*>(
           p.out + (static_cast<size_t>(it.qs + tq0 + tok) * p.H_q + it.h_kv * p.G + hh) * D);
@@ -641,6 +657,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const bool row_ok = tq0 + tok < it.t_end;
       const int row_pos = it.first_pos + tq0 + tok;
       const int row_lo = p.window > 0 ? max(0, row_pos - p.window + 1) : 0;
+      const int fcols = ANCH ? it.ab * PA_BLOCK_SIZE : 0;  // list columns of the anchors' own blocks
       float m_run = kNegInfTc, l_run = 0.f;
       for (int k = 0; ok && k < nt; ++k) {
         if (!warp_wait(&s_full[wg], sp & 1u)) {
@@ -653,7 +670,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * c));
         tmem_wait_ld();
-        const int kbase = (it.kb0 + 8 * k) * PA_BLOCK_SIZE;
+        const int kbase = (it.kb0 - (ANCH ? it.ab : 0) + 8 * k) * PA_BLOCK_SIZE;
         // scores stay raw (the scale is positive, so the maximum commutes with it); only tiles
         // that cross a row's causal or window edge take the per-key mask, and within them only
         // the 32-key chunks that some row of the warp attends in part (a row attends the tile's
@@ -662,7 +679,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // the keys past the item's last query on its diagonal tile) takes no maximum and no
         // exponentials: its P is zero.
         unsigned dead = 0;
-        if (!__all_sync(0xffffffffu, row_ok && kbase + 127 <= row_pos && kbase >= row_lo)) {
+        if constexpr (ANCH) {
+          // columns [0, an) are anchors, [lo, hi] the row's window; one interval when they meet
+          int lo = row_lo - kbase, an = row_ok ? p.anchors - 128 * k : 0;
+          const int hi = row_ok ? row_pos - kbase : -1;
+          if (an >= lo) lo = an = 0;
+          if (!__all_sync(0xffffffffu, lo <= 0 && hi >= 127)) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if (__all_sync(0xffffffffu, (lo <= 32 * q && hi >= 32 * q + 31) || an >= 32 * q + 32)) continue;
+              if (__all_sync(0xffffffffu, (hi < 32 * q || lo > 32 * q + 31) && an <= 32 * q)) {
+                dead |= 1u << q;
+                continue;
+              }
+#pragma unroll
+              for (int c = 32 * q; c < 32 * q + 32; ++c)
+                if ((c < lo || c > hi) && c >= an) sv[c] = __float_as_uint(kNegInfTc);
+            }
+          }
+        } else if (!__all_sync(0xffffffffu, row_ok && kbase + 127 <= row_pos && kbase >= row_lo)) {
           const int lo = row_lo - kbase, hi = row_ok ? row_pos - kbase : -1;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -693,8 +728,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         m_run = m_new;
         // key row r of V: zero it when it holds no loaded in-context data (both groups write the
         // same zeros; each must see them before its own P·V)
-        const int kp_r = kbase + r;
-        const bool zero_row = kp_r < it.kv_lo || kp_r >= it.loaded_end;
+        const int kp_r = ANCH && 128 * k + r < fcols ? 128 * k + r : kbase + r;
+        const bool zero_row = (kp_r < it.kv_lo && !(ANCH && kp_r < p.anchors)) || kp_r >= it.loaded_end;
         const int gk = g + k, vs = gk % kVStages;
         if (__any_sync(0xffffffffu, zero_row)) {
           // the stage's copies must have landed first
@@ -756,8 +791,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       bool bad = false;
       {
         const int32_t* trow = p.block_tables + static_cast<size_t>(it.s) * p.max_blocks;
-        for (int kb = it.kb0 + lane; kb < it.kb_end; kb += 32) {
-          const int e = trow[kb];
+        for (int b = lane; b < it.n_list; b += 32) {
+          const int e = trow[it.block(b)];
           bad |= e < 0 || e >= p.num_blocks;
         }
         bad = __any_sync(0xffffffffu, bad);
@@ -850,7 +885,7 @@ int resident_ctas() {
   if (dev < 64 && cached[dev] > 0) return cached[dev];
   int sms = 0, per_sm = 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, prefill_tc_kernel, kTcThreads, kTcSmem) != cudaSuccess ||
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, prefill_tc_kernel<false>, kTcThreads, kTcSmem) != cudaSuccess ||
       per_sm <= 0) {
     cudaGetLastError();
     per_sm = 1;
@@ -866,7 +901,7 @@ int resident_ctas() {
 pa_status launch_prefill_tc(const pa_cache_desc* desc, void* out, const void* q, const void* k_cache,
                             const void* v_cache, const int32_t* block_tables, const int32_t* q_start,
                             const int32_t* context_lens, int max_query_len, float scale, int32_t* err_flag,
-                            cudaStream_t stream, bool step) {
+                            cudaStream_t stream, bool step, int anchors) {
   const long long slots = static_cast<long long>(desc->num_blocks) * PA_BLOCK_SIZE;
   CUtensorMap mk, mv, mq, mo;
   const int G = desc->num_q_heads / desc->num_kv_heads;
@@ -884,6 +919,7 @@ pa_status launch_prefill_tc(const pa_cache_desc* desc, void* out, const void* q,
   p.max_blocks = desc->max_blocks_per_seq;
   p.max_q = max_query_len;
   p.window = desc->sliding_window;
+  p.anchors = anchors;
   p.tpq = 128 / p.G;
   p.step = step ? 1 : 0;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
@@ -893,7 +929,8 @@ pa_status launch_prefill_tc(const pa_cache_desc* desc, void* out, const void* q,
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.out = static_cast<__nv_bfloat16*>(out);
   p.err = err_flag;
-  if (!ensure_dynamic_smem(reinterpret_cast<const void*>(prefill_tc_kernel), kTcSmem)) return PA_ERR_CUDA;
+  auto kern = anchors > 0 && p.window > 0 ? prefill_tc_kernel<true> : prefill_tc_kernel<false>;
+  if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kern), kTcSmem)) return PA_ERR_CUDA;
   // Persistent CTAs: as many as run at once, but no more than there are work items, and enough
   // that none holds more than kMaxItems of them.
   const long long w_tokens = 2LL * p.tpq;  // query tokens of one tile
@@ -913,7 +950,7 @@ pa_status launch_prefill_tc(const pa_cache_desc* desc, void* out, const void* q,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefill_tc_kernel, mk, mv, mq, mo, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kern, mk, mv, mq, mo, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // namespace pa

@@ -43,11 +43,12 @@ EXPORTED = [
     "pa_status_string", "pa_kv_append", "pa_kv_append_tokens", "pa_block_copy",
     "pa_decode_workspace_size", "pa_decode_attention", "pa_decode_attention_noalloc", "pa_decode_step",
     "pa_decode_shared_workspace_size", "pa_decode_attention_shared",
+    "pa_decode_anchored_workspace_size", "pa_decode_attention_anchored",
     "pa_prefill_attention", "pa_prefill_step", "pa_prefill_workspace_size", "pa_prefill_attention_ws",
-    "pa_prefill_step_ws",
+    "pa_prefill_step_ws", "pa_prefill_anchored_workspace_size", "pa_prefill_attention_anchored",
     "pa_bm_create", "pa_bm_destroy", "pa_bm_alloc", "pa_bm_claim", "pa_bm_incref", "pa_bm_decref",
     "pa_bm_refcount", "pa_bm_num_free", "pa_bm_fork", "pa_bm_release", "pa_bm_prepare_step",
-    "pa_bm_slide_window",
+    "pa_bm_slide_window", "pa_bm_slide_window_anchored",
     "pa_pc_block_hashes", "pa_pc_create", "pa_pc_destroy", "pa_pc_match", "pa_pc_insert", "pa_pc_evict",
     "pa_pc_size", "pa_pc_clear",
 ]
@@ -121,6 +122,11 @@ def lib() -> ctypes.CDLL:
         L.pa_decode_attention_shared.restype = c_int
         L.pa_decode_attention_shared.argtypes = [dp, vp, vp, vp, vp, vp, vp, c_int, ctypes.c_float, c_int, vp,
                                                  c_int, c_int, vp, ctypes.c_size_t, vp, vp]
+        L.pa_decode_anchored_workspace_size.restype = ctypes.c_size_t
+        L.pa_decode_anchored_workspace_size.argtypes = [dp, c_int, c_int, c_int]
+        L.pa_decode_attention_anchored.restype = c_int
+        L.pa_decode_attention_anchored.argtypes = [dp, vp, vp, vp, vp, vp, vp, c_int, ctypes.c_float, c_int, c_int, vp,
+                                                   ctypes.c_size_t, vp, vp]
         L.pa_prefill_attention.restype = c_int
         L.pa_prefill_attention.argtypes = [dp, vp, vp, vp, vp, vp, vp, vp, c_int, ctypes.c_float, vp, vp]
         L.pa_prefill_workspace_size.restype = ctypes.c_size_t
@@ -128,6 +134,11 @@ def lib() -> ctypes.CDLL:
         L.pa_prefill_attention_ws.restype = c_int
         L.pa_prefill_attention_ws.argtypes = [dp, vp, vp, vp, vp, vp, vp, vp, c_int, c_int, ctypes.c_float, vp,
                                               ctypes.c_size_t, vp, vp]
+        L.pa_prefill_anchored_workspace_size.restype = ctypes.c_size_t
+        L.pa_prefill_anchored_workspace_size.argtypes = [dp, c_int, c_int, c_int]
+        L.pa_prefill_attention_anchored.restype = c_int
+        L.pa_prefill_attention_anchored.argtypes = [dp, vp, vp, vp, vp, vp, vp, vp, c_int, c_int, ctypes.c_float,
+                                                    c_int, vp, ctypes.c_size_t, vp, vp]
         L.pa_prefill_step_ws.restype = c_int
         L.pa_prefill_step_ws.argtypes = [dp, vp, vp, vp, vp, vp, vp, c_int, vp, vp, vp, vp, vp, c_int, c_int,
                                          ctypes.c_float, vp, ctypes.c_size_t, vp, vp]
@@ -161,6 +172,8 @@ def lib() -> ctypes.CDLL:
                                          ctypes.POINTER(c_int)]
         L.pa_bm_slide_window.restype = c_int
         L.pa_bm_slide_window.argtypes = [vp, vp, c_int, c_int, vp, c_int, ctypes.POINTER(c_int)]
+        L.pa_bm_slide_window_anchored.restype = c_int
+        L.pa_bm_slide_window_anchored.argtypes = [vp, vp, c_int, c_int, vp, c_int, c_int, ctypes.POINTER(c_int)]
         u64, u8p = ctypes.c_uint64, ctypes.POINTER(ctypes.c_uint8)
         L.pa_pc_block_hashes.restype = c_int
         L.pa_pc_block_hashes.argtypes = [i32p, c_int, u64, u64, u8p]
@@ -273,6 +286,25 @@ def pa_decode_attention_shared(desc, out, q, k_cache, v_cache, block_tables, con
            "pa_decode_attention_shared")
 
 
+def pa_decode_anchored_workspace_size(desc, max_context_len, partition_size=0, num_anchor=0) -> int:
+    return int(lib().pa_decode_anchored_workspace_size(ctypes.byref(desc), int(max_context_len),
+                                                       int(partition_size), int(num_anchor)))
+
+
+def pa_decode_attention_anchored(desc, out, q, k_cache, v_cache, block_tables, context_lens, max_context_len,
+                                 scale, partition_size, num_anchor, workspace, workspace_bytes=None, err_flag=None,
+                                 stream=None):
+    """pa_decode_attention over the window and the first num_anchor positions (see pa.h)."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check(lib().pa_decode_attention_anchored(ctypes.byref(desc), _ptr(out), _ptr(q), _ptr(k_cache),
+                                              _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
+                                              int(max_context_len), float(scale), int(partition_size),
+                                              int(num_anchor), _ptr(workspace), int(workspace_bytes),
+                                              _ptr(err_flag), _stream(stream)),
+           "pa_decode_attention_anchored")
+
+
 def pa_decode_step(desc, out, q, k_cache, v_cache, k_new, v_new, block_tables, positions, context_lens,
                    max_context_len, scale, partition_size, workspace, workspace_bytes=None, err_flag=None,
                    stream=None):
@@ -308,6 +340,25 @@ def pa_prefill_attention_ws(desc, out, q, k_cache, v_cache, block_tables, q_star
                                          int(max_query_len), int(max_context_len), float(scale), _ptr(workspace),
                                          int(workspace_bytes), _ptr(err_flag), _stream(stream)),
            "pa_prefill_attention_ws")
+
+
+def pa_prefill_anchored_workspace_size(desc, max_query_len, max_context_len, num_anchor) -> int:
+    return int(lib().pa_prefill_anchored_workspace_size(ctypes.byref(desc), int(max_query_len),
+                                                        int(max_context_len), int(num_anchor)))
+
+
+def pa_prefill_attention_anchored(desc, out, q, k_cache, v_cache, block_tables, q_start, context_lens, max_query_len,
+                                  max_context_len, scale, num_anchor, workspace, workspace_bytes=None, err_flag=None,
+                                  stream=None):
+    """pa_prefill_attention over the window and the first num_anchor positions (see pa.h)."""
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().pa_prefill_attention_anchored(ctypes.byref(desc), _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                               _ptr(block_tables), _ptr(q_start), _ptr(context_lens),
+                                               int(max_query_len), int(max_context_len), float(scale),
+                                               int(num_anchor), _ptr(workspace), int(workspace_bytes),
+                                               _ptr(err_flag), _stream(stream)),
+           "pa_prefill_attention_anchored")
 
 
 def pa_prefill_step_ws(desc, out, q, k_cache, v_cache, k_new, v_new, num_tokens, token_seq, token_pos, block_tables,
@@ -420,14 +471,16 @@ class BlockManager:
         _check(st, "pa_bm_prepare_step")
         return pairs[:n_pairs.value].copy(), n_changed.value
 
-    def slide_window(self, block_tables: np.ndarray, context_lens: np.ndarray, window: int):
-        """Release every block wholly before each sequence's window; returns (entries released,
-        blocks freed).  ``block_tables`` (int32 [B][max_blocks]) is updated in place."""
+    def slide_window(self, block_tables: np.ndarray, context_lens: np.ndarray, window: int, num_anchor: int = 0):
+        """Release every block wholly before each sequence's window, except those of its first
+        ``num_anchor`` positions; returns (entries released, blocks freed).  ``block_tables``
+        (int32 [B][max_blocks]) is updated in place."""
         bt = _i32(block_tables)
         ctx = _i32(np.ascontiguousarray(context_lens, dtype=np.int32))
         B, M = bt.shape
         n_freed = ctypes.c_int(0)
-        r = lib().pa_bm_slide_window(self._h, bt.ctypes.data, B, M, ctx.ctypes.data, int(window), ctypes.byref(n_freed))
+        r = lib().pa_bm_slide_window_anchored(self._h, bt.ctypes.data, B, M, ctx.ctypes.data, int(window),
+                                              int(num_anchor), ctypes.byref(n_freed))
         if r < 0:
             raise PaError(PA_ERR_INVALID_ARG, "pa_bm_slide_window")
         return r, n_freed.value
