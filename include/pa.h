@@ -287,6 +287,34 @@ pa_status pa_decode_attention_anchored(const pa_cache_desc* desc, void* out, con
                                        void* workspace, size_t workspace_bytes, int32_t* err_flag, void* stream);
 
 /* ---------------------------------------------------------------------------------
+ * Decode attention that accumulates attention weights (ldpk §5.3: a bounded cache keeps the positions
+ * that attention looks at most).  out is pa_decode_attention's, up to the order of the fp32 sums, and
+ * for every sequence s, KV head h and position t < ctx = context_lens[s]
+ *   scores_out[s][h][t] = scores_in[s][h][t] + sum over the G query heads of KV head h of their
+ *                         softmax weight of t (0 for a t before the sliding window)
+ * in fp32, sinks included.  pa_cache_evict takes the scores.
+ *   scores_in     device fp32 [num_seqs][num_kv_heads][score_stride], or NULL for zeros
+ *   scores_out    the same layout; it may be scores_in.  Entries at t >= ctx are left as they are, and
+ *                 so is the whole row of a sequence whose output a device error has zeroed.
+ *   score_stride  >= max_context_len
+ *   workspace     at least pa_decode_weights_workspace_size(desc, max_context_len, partition_size)
+ *                 bytes, 256-byte aligned, scratch for this call only: pa_decode_attention's and 4 bytes
+ *                 per (sequence, query head, position below max_context_len), G rounded up to a power
+ *                 of two.  The size is 0 when an argument is invalid.
+ * A query head whose softmax has no sum (no position, or NaN scores: its output row is zero) adds
+ * nothing.  Every cache kind; other arguments, device errors and host errors as pa_decode_attention;
+ * PA_ERR_UNSUPPORTED when num_kv_heads * ceil(max_context_len / 1024) passes what one launch takes
+ * (about 65000). */
+size_t pa_decode_weights_workspace_size(const pa_cache_desc* desc, int max_context_len, int partition_size);
+
+pa_status pa_decode_attention_weights(const pa_cache_desc* desc, void* out, const void* q,
+                                      const void* k_cache, const void* v_cache,
+                                      const int32_t* block_tables, const int32_t* context_lens,
+                                      int max_context_len, float scale, int partition_size,
+                                      const float* scores_in, float* scores_out, int score_stride,
+                                      void* workspace, size_t workspace_bytes, int32_t* err_flag, void* stream);
+
+/* ---------------------------------------------------------------------------------
  * Chunked-prefill (extend) attention over the paged cache (ldpk §2.2: under the causal mask the
  * query of position i attends to positions up to i; ldpk §7: long prompts are prefilled in
  * chunks).  Sequence s contributes the query rows q_start[s] .. q_start[s+1]-1 of q: they are its

@@ -32,6 +32,9 @@
 //    waits for it only before the blocks that receive the appended tokens.
 //  * With a shared prefix attended apart (pa_decode_attention_shared, shared_prefix.cu) a member
 //    sequence's list starts past the prefix, and the merge folds in the prefix's partial rows.
+//  * With accumulated weights (pa_decode_attention_weights) the consumers also store every attended
+//    position's scores (log2 units, fp32) to the workspace, and the merge launch carries more CTAs,
+//    which turn them into softmax weights once the row's maximum and sum are known (weights_rows).
 //  * Every wait is bounded; invalid table entries and contexts set error bits and zero rows.
 
 #include <algorithm>
@@ -108,6 +111,12 @@ struct DecodeParams {
   const float* extra;
   int shared_len;
   int n_extra;
+  // Scores of every attended position that is not a sink (pa_decode_attention_weights), or null:
+  // raw[((s * H_kv + h_kv) * raw_ctx + pos) * raw_g + g], in log2 units, for query head
+  // h_kv * G + g; raw_g is G rounded up to a power of two, so that a position's scores are one
+  // vector load.
+  float* raw;
+  int raw_ctx, raw_g;
 };
 
 // Blocks of a sequence with ctx tokens; -1 for an invalid context.
@@ -202,7 +211,8 @@ __device__ __forceinline__ Smem carve(uint8_t* raw, const DecodeParams& p) {
 // KIND 0: bf16 K and V; 1: FP8 E4M3 K and INT8 V with per-head scales; 2: INT4 K and V with a
 // scale and zero point per 32 dims of every token's head row; 3: as 1, but K with one scale per
 // token's head row (the block's scales follow its K and V tiles in the stage).
-template <int D, int KIND>
+// WT: the scores are stored for the attention weights (DecodeParams::raw).
+template <int D, int KIND, bool WT>
 struct Consumer {
   static constexpr bool QUANT = KIND == 1 || KIND == 3;
   static constexpr bool TOKS = KIND == 3;
@@ -468,9 +478,10 @@ struct Consumer {
 
   // Online-softmax update over NB blocks' scores at once (one maximum, one rescale check);
   // pr[b] = this lane's unnormalised probabilities {row t4: head 2tq, 2tq+1; row t4+8: same}.
+  // raw[b]: where the scores of block b's first token go (WT).
   template <int NB>
   __device__ __forceinline__ void softmax_n(const float (&acc)[NB][4], const int (&first)[NB], const int (&ntok)[NB],
-                                            float (&pr)[NB][4]) {
+                                            float (&pr)[NB][4], float* const (&raw)[NB]) {
     float s[NB][4];
     float bm0 = kNegInf, bm1 = kNegInf;
 #pragma unroll
@@ -481,6 +492,17 @@ struct Consumer {
       s[b][1] = v0 ? acc[b][1] * sl[1] : kNegInf;
       s[b][2] = v1 ? acc[b][2] * sl[0] : kNegInf;
       s[b][3] = v1 ? acc[b][3] * sl[1] : kNegInf;
+      if constexpr (WT) {
+        // 16 tokens x raw_g heads: a quad's lanes write consecutive heads of one token
+        if (p.raw_g == 1) {
+          if (tq == 0 && v0) raw[b][t4] = s[b][0];
+          if (tq == 0 && v1) raw[b][t4 + 8] = s[b][2];
+        } else if (2 * tq < p.raw_g) {
+          float2* r = reinterpret_cast<float2*>(raw[b] + t4 * p.raw_g + 2 * tq);
+          if (v0) r[0] = make_float2(s[b][0], s[b][1]);
+          if (v1) r[4 * p.raw_g] = make_float2(s[b][2], s[b][3]);
+        }
+      }
       bm0 = fmaxf(bm0, fmaxf(s[b][0], s[b][2]));
       bm1 = fmaxf(bm1, fmaxf(s[b][1], s[b][3]));
     }
@@ -585,35 +607,38 @@ struct Consumer {
   // One 16-token block: scores, online softmax update, P·V.
   // Tokens first .. ntok-1 of the block are attended; those below `first` are sink positions
   // (read from the bf16 sink buffer by the merge) or lie before the sliding window.
-  __device__ __forceinline__ void block(const uint8_t* stage, int first, int ntok) {
+  __device__ __forceinline__ void block(const uint8_t* stage, int first, int ntok, float* raw0) {
+    float* const raw[1] = {raw0};
     float acc[1][4], pr[1][4];
     const int f[1] = {first}, n[1] = {ntok};
     if constexpr (I4) {
       scores_i4(stage, acc[0]);
-      softmax_n<1>(acc, f, n, pr);
+      softmax_n<1>(acc, f, n, pr, raw);
       pv_i4(stage, pr[0], first, ntok);
     } else {
       scores(stage, acc[0]);
-      softmax_n<1>(acc, f, n, pr);
+      softmax_n<1>(acc, f, n, pr, raw);
       pv(stage, pr[0], first, ntok);
     }
   }
 
   // Two consecutive blocks of one sequence as one 32-token step: four independent q·Kᵀ chains,
   // one maximum and one rescale check for both, then both P·V products.
-  __device__ __forceinline__ void block2(const uint8_t* s0, int f0, int n0, const uint8_t* s1, int f1, int n1) {
+  __device__ __forceinline__ void block2(const uint8_t* s0, int f0, int n0, const uint8_t* s1, int f1, int n1,
+                                         float* raw0) {
+    float* const raw[2] = {raw0, WT ? raw0 + PA_BLOCK_SIZE * p.raw_g : raw0};  // consecutive logical blocks
     float acc[2][4], pr[2][4];
     const int f[2] = {f0, f1}, n[2] = {n0, n1};
     if constexpr (I4) {
       scores_i4(s0, acc[0]);
       scores_i4(s1, acc[1]);
-      softmax_n<2>(acc, f, n, pr);
+      softmax_n<2>(acc, f, n, pr, raw);
       pv_i4(s0, pr[0], f0, n0);
       pv_i4(s1, pr[1], f1, n1);
     } else {
       scores(s0, acc[0]);
       scores(s1, acc[1]);
-      softmax_n<2>(acc, f, n, pr);
+      softmax_n<2>(acc, f, n, pr, raw);
       pv(s0, pr[0], f0, n0);
       pv(s1, pr[1], f1, n1);
     }
@@ -826,7 +851,7 @@ __device__ __forceinline__ void drain_copies(const Smem& sm, int S, int from, in
   }
 }
 
-template <int D, int KIND, int MAXW>
+template <int D, int KIND, int MAXW, bool WT = false>
 __global__ void __launch_bounds__((MAXW + 1) * 32, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const __grid_constant__ CUtensorMap tmKp, const __grid_constant__ CUtensorMap tmVp,
@@ -961,7 +986,7 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1)
   // ------------------------------- consumers -------------------------------
   const int j = warp / p.hg;
   const int h_loc = warp - j * p.hg;
-  Consumer<D, KIND> c(p, lane, hgi * p.hg + h_loc, j, h_loc);
+  Consumer<D, KIND, WT> c(p, lane, hgi * p.hg + h_loc, j, h_loc);
   const int s_first = find_seq(sm.cum, nseq, u0);
   const int s_last = find_seq(sm.cum, nseq, u1 - 1);
   const int cta = blockIdx.x;
@@ -998,6 +1023,10 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1)
         c.bad = true;
       } else {
         const uint8_t* stage = sm.stages + static_cast<size_t>(st) * p.stage_bytes;
+        float* raw = nullptr;
+        if constexpr (WT)
+          raw = p.raw + ((static_cast<size_t>(seq_base + cur) * p.H_kv + c.h_kv) * p.raw_ctx +
+                         Producer<KIND>::logical(p, sm, cur, u) * PA_BLOCK_SIZE) * p.raw_g;
         if constexpr (MAXW <= 8) {
           // one block per stage: take the next stage too when its block belongs to the same
           // sequence, and run both as one 32-token step (every warp decides alike: the
@@ -1012,12 +1041,13 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1)
             }
             const int4 mt1 = sm.meta[st1];
             if (mt1.x == mt.x && !mt1.w) {
-              c.block2(stage, mt.y, mt.z, sm.stages + static_cast<size_t>(st1) * p.stage_bytes, mt1.y, mt1.z);
+              c.block2(stage, mt.y, mt.z, sm.stages + static_cast<size_t>(st1) * p.stage_bytes, mt1.y, mt1.z,
+                       raw);
               paired = true;
             }
           }
         }
-        if (!paired) c.block(stage, mt.y, mt.z);
+        if (!paired) c.block(stage, mt.y, mt.z, raw);
       }
     }
     __syncwarp();
@@ -1039,7 +1069,7 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1)
 // round: 8, or 16 when a shared prefix adds its rows (one round for both kinds).
 // ------------------------------------------------------------------------------------
 template <int D, int WPR, int CH>
-__global__ void __launch_bounds__(128) merge_kernel(const DecodeParams p, int grid_x) {
+__device__ __forceinline__ void merge_rows(const DecodeParams& p, int grid_x) {
   constexpr int E = D / 32;  // dims per lane
   const int s = blockIdx.x;
   const int wid = threadIdx.x >> 5;
@@ -1205,6 +1235,145 @@ __global__ void __launch_bounds__(128) merge_kernel(const DecodeParams p, int gr
   for (int e = 0; e < E; ++e) orow[lane * E + e] = __float2bfloat16_rn(acc[e] * inv);
 }
 
+template <int D, int WPR, int CH>
+__global__ void __launch_bounds__(128) merge_kernel(const DecodeParams p, int grid_x) {
+  merge_rows<D, WPR, CH>(p, grid_x);
+}
+
+// ------------------------------------------------------------------------------------
+// Accumulated attention weights: scores_out[s][h_kv][t] = scores_in[s][h_kv][t] + sum over the G query
+// heads of 2^(x_t - M) / L, x_t the stored scores, M and L the row's maximum and sum over all of its
+// partials and sinks.  Positions outside the attended range keep their score.  A CTA takes `chunk`
+// positions of one (sequence, KV head) and works M and L of its G rows out for itself: a few (m, l)
+// pairs each, all L2 hits.  It runs beside the merge's CTAs in one launch, as both need nothing but
+// the decode kernel.
+// ------------------------------------------------------------------------------------
+struct WeightsParams {
+  const float* scores_in;  // or null: zeros
+  float* scores_out;
+  int stride;   // scores of one (sequence, KV head) row
+  int chunk;    // positions per CTA
+  int merge_y;  // grid.y of the merge part
+  int chunks;   // CTAs per (sequence, KV head)
+};
+
+template <int D>
+__device__ __forceinline__ void weights_rows(const DecodeParams& p, const WeightsParams& wp, int grid_x, int h_kv,
+                                             int c0) {
+  constexpr int E = D / 32;
+  __shared__ float sh_m[8], sh_inv[8];
+  __shared__ int sh_bad;
+  const int s = blockIdx.x, tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
+  if (tid == 0) sh_bad = 0;
+  grid_dep_wait();
+  int cs = 0, ce = 0, T = 0;
+  if (p.mode == 0) {
+    cs = p.ws_meta[s];
+    ce = p.ws_meta[s + 1];
+    T = p.ws_meta[p.B + 1];
+  }
+  const int ctx = p.context_lens[s];
+  const int nb = seq_span(p, s, ctx);
+  if (nb < 0 || c0 >= ctx) return;
+  const int lo = seq_lo(p, s, ctx), n_sink = min(p.num_sink, ctx);
+  int c_first = 0, c_last = -1;
+  if (nb > 0) {
+    if (p.mode == 0) {
+      const int W = (T + grid_x - 1) / grid_x;
+      c_first = cs / W;
+      c_last = (ce - 1) / W;
+    } else {
+      c_last = (nb + p.ppb - 1) / p.ppb - 1;
+    }
+  }
+  const int n_parts = (c_last - c_first + 1) * p.nbs;
+  float* raw = p.raw + (static_cast<size_t>(s) * p.H_kv + h_kv) * p.raw_ctx * p.raw_g;
+  __syncthreads();
+  for (int g = wid; g < p.G; g += 4) {  // one warp per query head: M and L
+    const int h = h_kv * p.G + g;
+    float M = kNegInf, L = 0.f;
+    bool bad = false;
+    for (int i = lane; i < n_parts; i += 32) {
+      const int c = c_first + i / p.nbs, jj = i % p.nbs;
+      const size_t slot = p.mode == 0 ? static_cast<size_t>(s + c) : static_cast<size_t>(s) * p.max_parts + c;
+      const float* r = p.partials + ((slot * p.nbs + jj) * p.H_q + h) * static_cast<size_t>(D + 4) + D;
+      const float mi = r[0], li = r[1];
+      bad = bad || li < 0.f;
+      if (li > 0.f) {  // (a partial whose sum is NaN is left out, as by the merge)
+        const float mn = fmaxf(M, mi);
+        L = (M == kNegInf ? 0.f : L * ex2(M - mn)) + li * ex2(mi - mn);
+        M = mn;
+      }
+    }
+    float Mw = M;
+#pragma unroll
+    for (int mask = 1; mask < 32; mask <<= 1) Mw = warp_max_xor(Mw, mask);
+    float Lw = L != 0.f ? L * ex2(M - Mw) : 0.f;
+#pragma unroll
+    for (int mask = 1; mask < 32; mask <<= 1) Lw += __shfl_xor_sync(0xffffffffu, Lw, mask);
+    bad = __any_sync(0xffffffffu, bad);
+    if (n_sink > lo) {  // sinks: their scores, stored where this CTA takes them up below
+      const __nv_bfloat16* qrow = p.q + (static_cast<size_t>(s) * p.H_q + h) * D + lane * E;
+      float qv[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) qv[e] = __bfloat162float(qrow[e]);
+      for (int t = lo; t < n_sink; ++t) {
+        const __nv_bfloat16* krow = p.k_sink + ((static_cast<size_t>(s) * p.num_sink + t) * p.H_kv + h_kv) * D + lane * E;
+        float dot = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) dot += qv[e] * __bfloat162float(krow[e]);
+#pragma unroll
+        for (int mask = 1; mask < 32; mask <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, mask);
+        const float st = dot * p.scale_log2;
+        if (lane == 0 && t >= c0 && t < c0 + wp.chunk) raw[static_cast<size_t>(t) * p.raw_g + g] = st;
+        const float mn = fmaxf(Mw, st);
+        Lw = (Lw != 0.f ? Lw * ex2(Mw - mn) : 0.f) + ex2(st - mn);
+        Mw = mn;
+      }
+    }
+    if (lane == 0) {
+      sh_m[g] = Mw;
+      sh_inv[g] = Lw > 0.f ? 1.f / Lw : 0.f;  // no sum: the output row is zero, and so are its weights
+      if (bad) sh_bad = 1;
+    }
+  }
+  __syncthreads();
+  if (sh_bad) return;  // a table entry outside the pool: the row of scores is left as it was
+  const size_t row = (static_cast<size_t>(s) * p.H_kv + h_kv) * wp.stride;
+  const int end = min(ctx, c0 + wp.chunk);
+  auto weight = [&](float x, int g) {  // a score of NaN, or a row without a sum, adds nothing
+    const float e = ex2(x - sh_m[g]) * sh_inv[g];
+    return e > 0.f ? e : 0.f;
+  };
+#pragma unroll 4
+  for (int t = c0 + tid; t < end; t += 128) {
+    const float base = wp.scores_in ? wp.scores_in[row + t] : 0.f;
+    float w = 0.f;
+    if (t >= lo) {
+      const float* x = raw + static_cast<size_t>(t) * p.raw_g;
+      if (p.raw_g >= 4) {
+        for (int g = 0; g < p.G; g += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(x + g);
+          const float xs[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (g + e < p.G) w += weight(xs[e], g + e);
+        }
+      } else {
+        for (int g = 0; g < p.G; ++g) w += weight(x[g], g);
+      }
+    }
+    wp.scores_out[row + t] = base + w;  // (the step's weights summed first: one rounding into the score)
+  }
+}
+
+template <int D, int WPR>
+__global__ void __launch_bounds__(128) merge_weights_kernel(const DecodeParams p, const WeightsParams wp, int grid_x) {
+  const int y = static_cast<int>(blockIdx.y) - wp.merge_y;
+  if (y < 0) merge_rows<D, WPR, 8>(p, grid_x);
+  else weights_rows<D>(p, wp, grid_x, y / wp.chunks, (y % wp.chunks) * wp.chunk);
+}
+
 // ------------------------------------------------------------------------------------
 // Host side
 // ------------------------------------------------------------------------------------
@@ -1291,6 +1460,32 @@ pa_status make_plan(const pa_cache_desc* d, int max_ctx, int partition_size, Pla
   return PA_OK;
 }
 
+// positions of one CTA of the weights part
+constexpr int kWeightsChunk = 1024;
+
+template <int D, int KIND>
+pa_status launch_weights(const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mkp,
+                         const CUtensorMap& mvp, const DecodeParams& p, WeightsParams wp, cudaStream_t stream) {
+  auto kern = decode_kernel<D, KIND, 8, true>;
+  if (pl.warps_c > 8) {
+    if constexpr (KIND == 2) return PA_ERR_UNSUPPORTED;  // 4-bit plans have at most 8 consumer warps
+    else kern = decode_kernel<D, KIND, kMaxConsumerWarps, true>;
+  }
+  if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kern), pl.smem_bytes)) return PA_ERR_CUDA;
+  const dim3 grid = p.mode == 0 ? dim3(pl.grid_x, pl.n_hg, 1) : dim3(pl.max_parts, p.B, pl.n_hg);
+  if (launch_overlapped(kern, grid, dim3(pl.threads), pl.smem_bytes, stream, mk, mv, mkp, mvp, p) != PA_OK)
+    return PA_ERR_CUDA;
+  wp.chunk = kWeightsChunk;
+  wp.chunks = std::max(1, (p.max_ctx + wp.chunk - 1) / wp.chunk);
+  const bool few = static_cast<long long>(p.B) * p.H_q < 4LL * std::max(1, sm_count_current());
+  wp.merge_y = few ? p.H_q : (p.H_q + 3) / 4;
+  const long long ny = wp.merge_y + static_cast<long long>(p.H_kv) * wp.chunks;
+  if (ny > 65535) return PA_ERR_UNSUPPORTED;
+  const dim3 tail(p.B, static_cast<unsigned>(ny));
+  if (few) return launch_overlapped(merge_weights_kernel<D, 4>, tail, dim3(128), 0, stream, p, wp, pl.grid_x);
+  return launch_overlapped(merge_weights_kernel<D, 1>, tail, dim3(128), 0, stream, p, wp, pl.grid_x);
+}
+
 template <int D, int KIND>
 pa_status launch(const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mkp,
                  const CUtensorMap& mvp, const DecodeParams& p, cudaStream_t stream) {
@@ -1328,6 +1523,16 @@ extern "C" size_t pa_decode_workspace_size(const pa_cache_desc* desc, int max_co
 
 namespace pa {
 namespace {
+// Positions and heads that a stored row of scores is padded to (DecodeParams::raw).
+int raw_positions(int max_ctx) {
+  return static_cast<int>((static_cast<long long>(max_ctx) + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE * PA_BLOCK_SIZE);
+}
+int raw_heads(int G) {
+  int n = 1;
+  while (n < G) n *= 2;
+  return n;
+}
+
 // The prefix part of pa_decode_attention_shared, already enqueued: flags and rows as DecodeParams'.
 struct SharedPart {
   const int32_t* flags;
@@ -1337,12 +1542,14 @@ struct SharedPart {
 };
 
 // pa_decode_attention, the attention half of pa_decode_step (append_pos non-null), the decode half
-// of pa_decode_attention_shared (shared non-null) and pa_decode_attention_anchored (anchors > 0).
+// of pa_decode_attention_shared (shared non-null), pa_decode_attention_anchored (anchors > 0) and
+// pa_decode_attention_weights (weights non-null, raw its scores).
 pa_status decode_attention_impl(const pa_cache_desc* desc, void* out, const void* q, const void* k_cache,
                                 const void* v_cache, const int32_t* block_tables, const int32_t* context_lens,
                                 int max_context_len, float scale, int partition_size, void* workspace,
                                 size_t workspace_bytes, int32_t* err_flag, void* stream, const int32_t* append_pos,
-                                const SharedPart* shared = nullptr, int anchors = 0) {
+                                const SharedPart* shared = nullptr, int anchors = 0,
+                                const WeightsParams* weights = nullptr, float* raw = nullptr) {
   pa::Plan pl;
   pa_status st = pa::make_plan(desc, max_context_len, partition_size, &pl, anchors);
   if (st != PA_OK) return st;
@@ -1399,8 +1606,9 @@ pa_status decode_attention_impl(const pa_cache_desc* desc, void* out, const void
   p.mode = pl.mode;
   p.ppb = pl.ppb;
   p.max_parts = pl.max_parts;
-  // a row that one CTA covers is written by it, unless a shared prefix's rows are still to come
-  p.direct_ok = (pl.nbs == 1 && desc->num_sink == 0 && !shared) ? 1 : 0;
+  // a row that one CTA covers is written by it, unless a shared prefix's rows are still to come or
+  // its maximum and sum are wanted
+  p.direct_ok = (pl.nbs == 1 && desc->num_sink == 0 && !shared && !weights) ? 1 : 0;
   p.stage_bytes = pl.stage_bytes;
   p.block_bytes = pl.block_bytes;
   p.block_tx = pl.block_tx;
@@ -1421,9 +1629,20 @@ pa_status decode_attention_impl(const pa_cache_desc* desc, void* out, const void
   p.extra = shared ? shared->extra : nullptr;
   p.shared_len = shared ? shared->shared_len : 0;
   p.n_extra = shared ? shared->n_extra : 0;
+  p.raw = raw;
+  p.raw_ctx = raw_positions(max_context_len);
+  p.raw_g = raw_heads(p.G);
 
   cudaStream_t s = pa::as_stream(stream);
   const bool quant = pa::is_quantized(desc);
+  if (weights) {
+    if (desc->head_dim == 128)
+      return int4                         ? pa::launch_weights<128, 2>(pl, mk, mv, mkp, mvp, p, *weights, s)
+             : pa::has_token_scales(desc) ? pa::launch_weights<128, 3>(pl, mk, mv, mkp, mvp, p, *weights, s)
+             : quant                      ? pa::launch_weights<128, 1>(pl, mk, mv, mkp, mvp, p, *weights, s)
+                                          : pa::launch_weights<128, 0>(pl, mk, mv, mkp, mvp, p, *weights, s);
+    return pa::launch_weights<64, 0>(pl, mk, mv, mkp, mvp, p, *weights, s);
+  }
   if (desc->head_dim == 128)
     return int4                         ? pa::launch<128, 2>(pl, mk, mv, mkp, mvp, p, s)
            : pa::has_token_scales(desc) ? pa::launch<128, 3>(pl, mk, mv, mkp, mvp, p, s)
@@ -1485,6 +1704,55 @@ extern "C" pa_status pa_decode_attention_anchored(const pa_cache_desc* desc, voi
   return pa::decode_attention_impl(desc, out, q, k_cache, v_cache, block_tables, context_lens, max_context_len,
                                    scale, partition_size, workspace, workspace_bytes, err_flag, stream, nullptr,
                                    nullptr, num_anchor);
+}
+
+// ------------------------------------------------------------------------------------
+// Decode attention with accumulated weights: the decode kernel's workspace, then the scores.
+// ------------------------------------------------------------------------------------
+namespace pa {
+namespace {
+bool weights_layout(const pa_cache_desc* desc, int max_context_len, int partition_size, size_t* raw_off,
+                    size_t* total) {
+  Plan pl;
+  if (make_plan(desc, max_context_len, partition_size, &pl) != PA_OK || max_context_len > 0x7FFFFF00) return false;
+  *raw_off = (pl.ws_bytes + 255) / 256 * 256;
+  *total = *raw_off + static_cast<size_t>(desc->num_seqs) * desc->num_kv_heads * raw_positions(max_context_len) *
+                          raw_heads(desc->num_q_heads / desc->num_kv_heads) * sizeof(float);
+  return true;
+}
+}  // namespace
+}  // namespace pa
+
+extern "C" size_t pa_decode_weights_workspace_size(const pa_cache_desc* desc, int max_context_len,
+                                                   int partition_size) {
+  size_t raw_off = 0, total = 0;
+  return pa::weights_layout(desc, max_context_len, partition_size, &raw_off, &total) ? total : 0;
+}
+
+extern "C" pa_status pa_decode_attention_weights(const pa_cache_desc* desc, void* out, const void* q,
+                                                 const void* k_cache, const void* v_cache,
+                                                 const int32_t* block_tables, const int32_t* context_lens,
+                                                 int max_context_len, float scale, int partition_size,
+                                                 const float* scores_in, float* scores_out, int score_stride,
+                                                 void* workspace, size_t workspace_bytes, int32_t* err_flag,
+                                                 void* stream) {
+  pa::Plan pl;
+  const pa_status st = pa::make_plan(desc, max_context_len, partition_size, &pl);
+  if (st != PA_OK) return st;
+  size_t raw_off = 0, total = 0;
+  if (!pa::weights_layout(desc, max_context_len, partition_size, &raw_off, &total)) return PA_ERR_INVALID_ARG;
+  if (score_stride < max_context_len) return PA_ERR_INVALID_ARG;
+  if (desc->num_seqs == 0) return PA_OK;
+  if (!scores_out || !workspace || ((reinterpret_cast<uintptr_t>(scores_in) | reinterpret_cast<uintptr_t>(scores_out)) & 3u))
+    return PA_ERR_INVALID_ARG;
+  if (workspace_bytes < total) return PA_ERR_WORKSPACE_TOO_SMALL;
+  pa::WeightsParams wp = {};
+  wp.scores_in = scores_in;
+  wp.scores_out = scores_out;
+  wp.stride = score_stride;
+  return pa::decode_attention_impl(desc, out, q, k_cache, v_cache, block_tables, context_lens, max_context_len,
+                                   scale, partition_size, workspace, raw_off, err_flag, stream, nullptr, nullptr, 0,
+                                   &wp, reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + raw_off));
 }
 
 // ------------------------------------------------------------------------------------

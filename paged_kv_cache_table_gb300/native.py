@@ -44,6 +44,7 @@ EXPORTED = [
     "pa_decode_workspace_size", "pa_decode_attention", "pa_decode_attention_noalloc", "pa_decode_step",
     "pa_decode_shared_workspace_size", "pa_decode_attention_shared",
     "pa_decode_anchored_workspace_size", "pa_decode_attention_anchored",
+    "pa_decode_weights_workspace_size", "pa_decode_attention_weights",
     "pa_prefill_attention", "pa_prefill_step", "pa_prefill_workspace_size", "pa_prefill_attention_ws",
     "pa_prefill_step_ws", "pa_prefill_anchored_workspace_size", "pa_prefill_attention_anchored",
     "pa_bm_create", "pa_bm_destroy", "pa_bm_alloc", "pa_bm_claim", "pa_bm_incref", "pa_bm_decref",
@@ -127,6 +128,11 @@ def lib() -> ctypes.CDLL:
         L.pa_decode_attention_anchored.restype = c_int
         L.pa_decode_attention_anchored.argtypes = [dp, vp, vp, vp, vp, vp, vp, c_int, ctypes.c_float, c_int, c_int, vp,
                                                    ctypes.c_size_t, vp, vp]
+        L.pa_decode_weights_workspace_size.restype = ctypes.c_size_t
+        L.pa_decode_weights_workspace_size.argtypes = [dp, c_int, c_int]
+        L.pa_decode_attention_weights.restype = c_int
+        L.pa_decode_attention_weights.argtypes = [dp, vp, vp, vp, vp, vp, vp, c_int, ctypes.c_float, c_int, vp, vp,
+                                                  c_int, vp, ctypes.c_size_t, vp, vp]
         L.pa_prefill_attention.restype = c_int
         L.pa_prefill_attention.argtypes = [dp, vp, vp, vp, vp, vp, vp, vp, c_int, ctypes.c_float, vp, vp]
         L.pa_prefill_workspace_size.restype = ctypes.c_size_t
@@ -303,6 +309,25 @@ def pa_decode_attention_anchored(desc, out, q, k_cache, v_cache, block_tables, c
                                               int(num_anchor), _ptr(workspace), int(workspace_bytes),
                                               _ptr(err_flag), _stream(stream)),
            "pa_decode_attention_anchored")
+
+
+def pa_decode_weights_workspace_size(desc, max_context_len, partition_size=0) -> int:
+    return int(lib().pa_decode_weights_workspace_size(ctypes.byref(desc), int(max_context_len),
+                                                      int(partition_size)))
+
+
+def pa_decode_attention_weights(desc, out, q, k_cache, v_cache, block_tables, context_lens, max_context_len, scale,
+                                partition_size, scores_in, scores_out, score_stride, workspace, workspace_bytes=None,
+                                err_flag=None, stream=None):
+    """pa_decode_attention that also adds every position's attention weight to its score (see pa.h)."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check(lib().pa_decode_attention_weights(ctypes.byref(desc), _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                             _ptr(block_tables), _ptr(context_lens), int(max_context_len),
+                                             float(scale), int(partition_size), _ptr(scores_in), _ptr(scores_out),
+                                             int(score_stride), _ptr(workspace), int(workspace_bytes),
+                                             _ptr(err_flag), _stream(stream)),
+           "pa_decode_attention_weights")
 
 
 def pa_decode_step(desc, out, q, k_cache, v_cache, k_new, v_new, block_tables, positions, context_lens,

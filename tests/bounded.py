@@ -93,3 +93,32 @@ def decode_anchored(g, q, ctx, anchors, partition=0, ws_fill=0xFF, max_ctx=None)
     N.pa_decode_attention_anchored(g.desc, out, q.cuda(), g.k, g.v, g.tables_dev, gpu(ctx), max_ctx, w.scale, partition,
                                    anchors, ws, n, g.err)
     return out
+
+
+def decode_weights(g, q, ctx, scores_in, scores_out, partition=0, ws_fill=0xFF, max_ctx=None):
+    """pa_decode_attention_weights; scores as fp32 device tensors [B][H_kv][stride] (scores_in may be None)."""
+    w = g.w
+    max_ctx = int(max(ctx)) if max_ctx is None else max_ctx
+    out = torch.full((w.B, w.H_q, w.D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    n = N.pa_decode_weights_workspace_size(g.desc, max_ctx, partition)
+    assert n > 0
+    ws = torch.full((n,), ws_fill, dtype=torch.uint8, device="cuda")
+    N.pa_decode_attention_weights(g.desc, out, q.cuda(), g.k, g.v, g.tables_dev, gpu(ctx), max_ctx, w.scale, partition,
+                                  scores_in, scores_out, scores_out.shape[2], ws, n, g.err)
+    return out
+
+
+def weight_tolerance(weights, base, q, K, scale, kmag=None):
+    """How far accumulated fp32 weights may be off.  A score is a sum of D exact products in fp32, off by
+    at most D 2^-23 of the sum of |q k|, and is scaled and rounded (2^-22 of it); a weight is off by twice
+    that (its own score and the sum's) and by the exponentials', the sum's and the division's roundings,
+    under 2^-19.  kmag: the largest |code| that 4-bit keys enter the products with, in place of |K|.
+    The running score is rounded once or twice more."""
+    G = q.shape[0] // K.shape[1]
+    tol = np.zeros_like(weights)
+    for h in range(K.shape[1]):
+        a = np.abs(q[h * G:(h + 1) * G])
+        mag = scale * (np.abs(K[:, h]) @ a.T if kmag is None else np.full((len(K), G), kmag) * a.sum(1))
+        d = mag.max(initial=0.0) * (K.shape[2] + 4) * 2.0 ** -23
+        tol[h] = weights[h] * (2 * d + 2.0 ** -19) + 2.0 ** -22 * np.abs(base[h] + weights[h]) + 1e-30
+    return tol
