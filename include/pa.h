@@ -29,6 +29,9 @@
  *     (pa_decode_attention_anchored, pa_prefill_attention_anchored), and their blocks stay in the
  *     pool (pa_bm_slide_window_anchored).  显存账本 §七 keeps the first tokens because attention gathers
  *     there; dropped from a window they take most of the softmax mass with them.
+ *   - Optional eviction: decode attention can add every position's softmax weight to a running score
+ *     (pa_decode_attention_weights), and pa_cache_evict keeps the budget of best-scored, first and
+ *     most recent tokens per KV head, compacting the cache in place.
  *   - Sequences that share a prompt prefix point their tables at one copy of its whole blocks
  *     (AI内存系统 §3.1, §3.3); pa_decode_attention_shared attends those blocks once for all of
  *     them and merges that part with each sequence's own positions.
@@ -477,6 +480,49 @@ pa_status pa_decode_step(const pa_cache_desc* desc, void* out, const void* q, vo
                          const int32_t* context_lens, int max_context_len, float scale,
                          int partition_size, void* workspace, size_t workspace_bytes,
                          int32_t* err_flag, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * Eviction by accumulated attention weight (ldpk §5.3: a bounded cache keeps the positions that
+ * attention looks at most and the most recent ones; 显存账本 §七: the first tokens stay).  For every
+ * sequence s and KV head h, with n = context_lens[s] slots in use, holding the tokens at positions
+ * pos_in[s][h][0 .. n-1], and newest = the largest of those positions:
+ *   protected  the slots with position < num_anchor or position > newest - num_recent;
+ *   kept       if n > budget: budget slots, the protected ones first, then by score from the highest
+ *              (NaN last), equal scores by slot from the lowest; else all n;
+ *   new length left = min(n, budget), the same for all heads: the caller's next context length.
+ * The cache is compacted in place: kept slots below left stay, and the i-th evicted slot below left
+ * receives the row (K and V codes, parameters and scales), score and position of the i-th kept slot at
+ * or past left.  So the slots of different heads hold different tokens, and a head's slots are not in
+ * order of position; decode attention does not depend on either.  Then
+ *   scores_out[s][h][j], pos_out[s][h][j]   for j < left: of the token now in slot j; for left <= j <
+ *              stride: 0 and newest + 1 + (j - left), i.e. what the tokens appended next need.
+ * The caller releases the blocks past the new length (pa_bm_release on entries ceil(left/16) ..), takes
+ * left as the length that appends continue at, and keeps counting true positions itself (for rotary
+ * embeddings).  Nothing is written outside slots < left of the cache.
+ *   scores_in, scores_out   device fp32 [num_seqs][num_kv_heads][stride], as pa_decode_attention_weights
+ *   pos_in, pos_out         device int32, the same layout; pos_in NULL: slot j holds position j (a cache
+ *                           never evicted from).  *_out may be *_in; buffers must not overlap otherwise.
+ *   max_context_len         bounds every context_lens[s]; stride >= max_context_len
+ *   budget >= 1, num_recent >= 0, num_anchor >= desc->num_sink (rows in the sink buffers are not
+ *   moved), num_anchor + num_recent <= budget
+ *   workspace               at least pa_cache_evict_workspace_size(desc, max_context_len, budget) bytes,
+ *                           256-byte aligned, scratch for this call only.  The size is 0 when an
+ *                           argument is invalid.
+ * Blocks that hold a slot below left of a sequence with n > budget must not be shared with another
+ * sequence (their rows change): copy them first (pa_bm_prepare_step at one position of each, then
+ * pa_block_copy).
+ * A context that is negative, beyond the table or beyond max_context_len sets PA_EFLAG_CTX_OVERFLOW and
+ * leaves the sequence as it was, its scores_out and pos_out rows too; a table entry outside
+ * [0, num_blocks) under a moved row sets PA_EFLAG_BAD_BLOCK_ID and skips that row's K and V.
+ * Every cache kind; desc->sliding_window > 0 gives PA_ERR_UNSUPPORTED.
+ * Host errors: PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE_TOO_SMALL, PA_ERR_CUDA. */
+size_t pa_cache_evict_workspace_size(const pa_cache_desc* desc, int max_context_len, int budget);
+
+pa_status pa_cache_evict(const pa_cache_desc* desc, void* k_cache, void* v_cache,
+                         const int32_t* block_tables, const int32_t* context_lens, int max_context_len,
+                         const float* scores_in, float* scores_out, const int32_t* pos_in, int32_t* pos_out,
+                         int stride, int budget, int num_anchor, int num_recent,
+                         void* workspace, size_t workspace_bytes, int32_t* err_flag, void* stream);
 
 /* ---------------------------------------------------------------------------------
  * Host block manager: the physical block pool with a free list and reference counts

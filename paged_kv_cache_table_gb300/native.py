@@ -47,6 +47,7 @@ EXPORTED = [
     "pa_decode_weights_workspace_size", "pa_decode_attention_weights",
     "pa_prefill_attention", "pa_prefill_step", "pa_prefill_workspace_size", "pa_prefill_attention_ws",
     "pa_prefill_step_ws", "pa_prefill_anchored_workspace_size", "pa_prefill_attention_anchored",
+    "pa_cache_evict_workspace_size", "pa_cache_evict",
     "pa_bm_create", "pa_bm_destroy", "pa_bm_alloc", "pa_bm_claim", "pa_bm_incref", "pa_bm_decref",
     "pa_bm_refcount", "pa_bm_num_free", "pa_bm_fork", "pa_bm_release", "pa_bm_prepare_step",
     "pa_bm_slide_window", "pa_bm_slide_window_anchored",
@@ -155,6 +156,11 @@ def lib() -> ctypes.CDLL:
         L.pa_decode_attention_noalloc.argtypes = [dp, vp, vp, vp, vp, vp, vp, c_int, ctypes.c_float, c_int, vp, vp]
         L.pa_decode_step.restype = c_int
         L.pa_decode_step.argtypes = [dp, vp, vp, vp, vp, vp, vp, vp, vp, vp, c_int, ctypes.c_float, c_int, vp,
+                                     ctypes.c_size_t, vp, vp]
+        L.pa_cache_evict_workspace_size.restype = ctypes.c_size_t
+        L.pa_cache_evict_workspace_size.argtypes = [dp, c_int, c_int]
+        L.pa_cache_evict.restype = c_int
+        L.pa_cache_evict.argtypes = [dp, vp, vp, vp, vp, c_int, vp, vp, vp, vp, c_int, c_int, c_int, c_int, vp,
                                      ctypes.c_size_t, vp, vp]
         L.pa_bm_create.restype = vp
         L.pa_bm_create.argtypes = [c_int, c_int]
@@ -418,6 +424,24 @@ def pa_decode_attention_noalloc(desc, out, q, k_cache, v_cache, block_tables, co
                                              int(max_context_len), float(scale), int(partition_size),
                                              _ptr(err_flag), _stream(stream)),
            "pa_decode_attention_noalloc")
+
+
+def pa_cache_evict_workspace_size(desc, max_context_len, budget) -> int:
+    return int(lib().pa_cache_evict_workspace_size(ctypes.byref(desc), int(max_context_len), int(budget)))
+
+
+def pa_cache_evict(desc, k_cache, v_cache, block_tables, context_lens, max_context_len, scores_in, scores_out, pos_in,
+                   pos_out, stride, budget, num_anchor, num_recent, workspace, workspace_bytes=None, err_flag=None,
+                   stream=None):
+    """Keep the budget of best-scored, first and recent tokens of every sequence and KV head (see pa.h)."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check(lib().pa_cache_evict(ctypes.byref(desc), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+                                _ptr(context_lens), int(max_context_len), _ptr(scores_in), _ptr(scores_out),
+                                _ptr(pos_in), _ptr(pos_out), int(stride), int(budget), int(num_anchor),
+                                int(num_recent), _ptr(workspace), int(workspace_bytes), _ptr(err_flag),
+                                _stream(stream)),
+           "pa_cache_evict")
 
 
 def _i32(a) -> np.ndarray:

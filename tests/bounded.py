@@ -122,3 +122,32 @@ def weight_tolerance(weights, base, q, K, scale, kmag=None):
         d = mag.max(initial=0.0) * (K.shape[2] + 4) * 2.0 ** -23
         tol[h] = weights[h] * (2 * d + 2.0 ** -19) + 2.0 ** -22 * np.abs(base[h] + weights[h]) + 1e-30
     return tol
+
+
+def evict(g, ctx, scores_in, scores_out, pos_in, pos_out, budget, anchors, recent, max_ctx=None, ws_fill=0xFF):
+    max_ctx = int(max(ctx)) if max_ctx is None else max_ctx
+    n = N.pa_cache_evict_workspace_size(g.desc, max_ctx, budget)
+    assert n > 0
+    ws = torch.full((n,), ws_fill, dtype=torch.uint8, device="cuda")
+    N.pa_cache_evict(g.desc, g.k, g.v, g.tables_dev, gpu(ctx), max_ctx, scores_in, scores_out, pos_in, pos_out,
+                     scores_in.shape[2], budget, anchors, recent, ws, n, g.err)
+
+
+def oracle_evict(o, ctx, scores, pos, stride, budget, anchors, recent):
+    """The same on the oracle's cache; scores and pos [B][H_kv][stride] (pos may be None).  Returns the
+    expected (scores_out, pos_out)."""
+    B, H = scores.shape[:2]
+    so, po = np.zeros((B, H, stride), np.float32), np.zeros((B, H, stride), np.int64)
+    for s in range(B):
+        n = int(ctx[s])
+        left = min(n, budget)
+        for h in range(H):
+            sc = scores[s, h, :n]
+            ps = np.arange(n) if pos is None else pos[s, h, :n].astype(np.int64)
+            holes, movers = O.evict_plan(sc, ps, budget, anchors, recent)
+            O.evict_rows(o.cache, o.tables[s], h, holes, movers)
+            place = np.arange(left)
+            place[holes] = movers
+            so[s, h, :left], po[s, h, :left] = sc[place], ps[place]
+            po[s, h, left:] = (ps.max() if n else -1) + 1 + np.arange(stride - left)
+    return so, po
