@@ -13,17 +13,25 @@
 // been overwritten, in place or not.  The heads of a token part company: slot j of head h holds the
 // token at position token_pos[s][h][j].
 //
-// Design (one launch).  A cluster of C CTAs takes one (sequence, KV head); a CTA owns a run of slots
-// and a warp a run of those, in order, so that ranks in slot order need only ballots and prefix sums.
+// Design.  A cluster of C CTAs takes one (sequence, KV head); a CTA owns a run of slots and a warp a run
+// of those, in order, so that ranks in slot order need only ballots and prefix sums.
 //  1. newest position (maximum over the slots), needed to know which slots are recent;
-//  2. keys: the score as an order-preserving 32-bit integer (protected: all ones, NaN: 0) in shared
-//     memory, as many as fit; the others are made again from the scores at each pass;
-//  3. the b-th largest key by radix selection, digits of 11, 11 and 10 bits: shared-memory histograms,
-//     summed over the cluster through distributed shared memory;
-//  4. slots equal to it are kept in slot order up to the budget (ranks only when some must go);
-//  5. holes and movers are counted and ranked; their physical slots go to two lists in the workspace;
-//     the kept scores and positions are written, and those past the new length;
-//  6. the cluster moves the listed rows, 16 bytes per thread and access.
+//  2. keys: the score as an order-preserving 32-bit integer (protected: all ones, NaN: 0), kept in shared
+//     memory, as many as fit; the others are made again at each pass;
+//  3. the b-th largest key by radix selection, digits of 12, 10 and 10 bits: shared-memory histograms,
+//     summed over the cluster through distributed shared memory, each CTA taking its share of the bins
+//     (12 bits: the sign, the exponent and three bits of the mantissa spread accumulated weights, which
+//     range over many octaves, over enough bins that the lanes of a warp seldom meet in one).  After the
+//     first digit the keys that share it, a few of a hundred, are put in a list for the other two;
+//  4. slots equal to it are kept in slot order up to the budget (ranks only when some must go); one word
+//     of kept bits per 32 slots;
+//  5. holes and movers are counted and ranked, one lane per word, and their physical slots go to two lists
+//     in the workspace, one lane per slot (a store of consecutive entries); scores and positions of kept
+//     slots are copied (unless in place);
+//  6. movers' scores and positions go to the holes, and the listed rows move, 16 bytes per lane: a lane's
+//     part of a row (which tensor, which 16 bytes) is the same for every row, and a warp has several rows
+//     in flight.  With many slots per CTA there are few CTAs and many rows, and a second launch with as
+//     many CTAs as the GPU holds moves them.
 // Everything is integer comparison and counting in a fixed order: the result does not depend on timing.
 
 #include <algorithm>
@@ -34,19 +42,16 @@
 namespace pa {
 namespace {
 
-constexpr int kEvThreads = 512;
-constexpr int kEvWarps = kEvThreads / 32;
-constexpr int kEvBins = 2048;
+constexpr int kEvBins = 4096;
+constexpr int kEvList = 1024;     // keys of the list after the first digit; more: all keys are gone over again
 constexpr int kEvMaxCluster = 8;  // the portable cluster size
-// slots per CTA that a cluster is made larger for
-#ifndef PA_EVICT_SPAN
-#define PA_EVICT_SPAN 4096
-#endif
-constexpr size_t kEvMaxKeyBytes = 192 * 1024;  // dynamic shared memory for keys, beside the histograms
+constexpr int kEvSmall = 4096;     // slots up to which a CTA has 256 threads and keeps scores and positions
+constexpr int kEvMaxKeys = 40960;  // keys kept in shared memory otherwise
+constexpr int kEvMaxContext = 1 << 21;  // so that every word of kept bits has its place in shared memory too
 
 struct EvictParams {
   int B, H, num_blocks, max_blocks, max_ctx, stride, budget, anchors, recent;
-  int cluster, key_cap, max_moves;
+  int cluster, cap, max_moves;
   const int32_t* block_tables;
   const int32_t* context_lens;
   const float* scores_in;
@@ -54,7 +59,8 @@ struct EvictParams {
   const int32_t* pos_in;  // or null: slot j holds position j
   int32_t* pos_out;
   int2* holes;   // [B * H][max_moves] (physical slot or -1, slot)
-  int4* movers;  // [B * H][max_moves] (physical slot or -1, score bits, position, 0)
+  int2* movers;  // the same
+  int* counts;   // [B * H] rows to move (when a second launch moves them)
   // a (slot, head) row in 16-byte units: K codes, V codes, K parameters, V parameters (INT4)
   uint4* part[4];
   int units[4], total_units;
@@ -81,6 +87,11 @@ __device__ __forceinline__ int remote_ld(const int* p, int rank) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return static_cast<int>(v);
 }
+__device__ __forceinline__ void remote_st(int* p, int rank, int v) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
 
 __device__ __forceinline__ uint32_t score_key(float x) {
   if (x != x) return 0u;
@@ -88,38 +99,116 @@ __device__ __forceinline__ uint32_t score_key(float x) {
   return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive prefix over the warps of a CTA and the CTAs before it of v (one value per warp, valid in
-// lane 0); `total` receives the cluster's sum.  `tot` and `sh` are this quantity's own shared words.
-__device__ __forceinline__ int warp_prefix(int v, int* sh, int* tot, int warp, int lane, int rank, int cluster,
-                                           int* total) {
-  if (lane == 0) sh[warp] = v;
-  __syncthreads();
-  int before = 0, all = 0;
-  for (int w = 0; w < kEvWarps; ++w) {
-    before += w < warp ? sh[w] : 0;
-    all += sh[w];
-  }
-  if (cluster > 1) {
-    if (threadIdx.x == 0) *tot = all;
-    cluster_sync_all(cluster);
-    int sum = 0;
-    for (int c = 0; c < cluster; ++c) {
-      const int x = remote_ld(tot, c);
-      before += c < rank ? x : 0;
-      sum += x;
-    }
-    all = sum;
-  }
-  *total = all;
-  return before;
+// Bits 0 .. n - 1, n clamped to 0 .. 32.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u); }
+
+// Bins are scanned by the thread that holds kEvRun consecutive ones; bin b lies at (b % kEvRun) *
+// kEvPitch + b / kEvRun, so that neither this scan (threads at consecutive words) nor neighbouring
+// bins hit by a warp's atomics (kEvPitch is odd) meet in a bank.
+constexpr int kEvRun = 16, kEvRuns = kEvBins / kEvRun, kEvPitch = kEvRuns + 1;
+__device__ __forceinline__ int bin_at(int b) { return (b & (kEvRun - 1)) * kEvPitch + (b / kEvRun); }
+
+template <int T>
+struct EvictShared {
+  alignas(16) int hist[kEvRun * kEvPitch];
+  int runs[kEvRuns];  // keys in this CTA's share of the runs of bins, over the cluster
+  uint32_t list[kEvList];
+  int above_warp[T / 32];
+  int warp[3][T / 32];
+  int tot[3];
+  int slice[kEvMaxCluster];  // keys counted in each CTA's share of the bins
+  int max, run, above, digit, rest, count, listed;
+};
+
+// Sum over the warps of a CTA of v[w], and of those before (or, `after`, behind) this one; every lane.
+template <int W>
+__device__ __forceinline__ int warps_sum(const int* v, int* part, bool after) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int x = lane < W ? v[lane] : 0;
+  *part = __reduce_add_sync(0xffffffffu, (after ? lane > warp : lane < warp) ? x : 0);
+  return __reduce_add_sync(0xffffffffu, x);
 }
 
-__global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictParams p) {
-  extern __shared__ uint32_t keys[];
-  __shared__ int hist[kEvBins], above_warp[kEvWarps];
-  __shared__ int sh_warp[3][kEvWarps];
-  __shared__ int sh_tot[3];
-  __shared__ int sh_max, sh_digit, sh_rest, sh_count;
+// Exclusive prefix, over the warps of a CTA and the CTAs before it, of N quantities that lane 0 of each
+// warp holds; total[] receives the cluster's sums.  sh.warp[q0 ..] and sh.tot[q0 ..] are theirs alone.
+template <int T, int N>
+__device__ __forceinline__ void warp_prefix(EvictShared<T>& sh, int q0, const int (&v)[N], int (&before)[N],
+                                            int (&total)[N], int rank, int cluster) {
+  const int warp = threadIdx.x >> 5;
+  if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+    for (int q = 0; q < N; ++q) sh.warp[q0 + q][warp] = v[q];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < N; ++q) total[q] = warps_sum<T / 32>(sh.warp[q0 + q], &before[q], false);
+  if (cluster > 1) {
+    if (threadIdx.x == 0) {
+#pragma unroll
+      for (int q = 0; q < N; ++q) sh.tot[q0 + q] = total[q];
+    }
+    cluster_sync_all(cluster);
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      total[q] = 0;
+      for (int c = 0; c < cluster; ++c) {
+        const int x = remote_ld(&sh.tot[q0 + q], c);
+        before[q] += c < rank ? x : 0;
+        total[q] += x;
+      }
+    }
+  }
+}
+
+// Rows of the lists of one (sequence, head) that warp `w` of `nw` moves: 16 bytes per lane and row, four
+// rows in flight.  (Loading 32 list entries at once, one per lane, and shuffling them out was slower: 46
+// against 38 us for the 128 pairs of up to 8192 slots.)
+__device__ __forceinline__ void move_rows(const EvictParams& p, int pair, int moves, int w, int nw) {
+  const int lane = threadIdx.x & 31, h = pair % p.H;
+  const int2* holes = p.holes + static_cast<size_t>(pair) * p.max_moves;
+  const int2* movers = p.movers + static_cast<size_t>(pair) * p.max_moves;
+  // a lane's 16 bytes of every row it takes: tensor t, unit r of row `sub` of the warp's `group` rows
+  const int group = 32 / p.total_units, sub = lane / p.total_units;
+  int r = lane - sub * p.total_units, t = 0;
+  while (t < 3 && r >= p.units[t]) r -= p.units[t++];
+  uint4* base = p.part[t] + static_cast<size_t>(h) * p.units[t] + r;
+  const size_t step = static_cast<size_t>(p.H) * p.units[t];  // from one slot's row of this head to the next's
+  constexpr int kDepth = 4;
+  const int stride_rows = nw * group;
+  for (int i0 = w * group + sub; i0 < moves; i0 += stride_rows * kDepth) {
+    uint4 v[kDepth];
+    int to[kDepth], from[kDepth];
+#pragma unroll
+    for (int e = 0; e < kDepth; ++e) {
+      const int i = i0 + e * stride_rows;
+      const bool on = sub < group && i < moves;
+      to[e] = on ? holes[i].x : -1;
+      from[e] = on ? movers[i].x : -1;
+    }
+#pragma unroll
+    for (int e = 0; e < kDepth; ++e)  // (negative: a table entry outside the pool)
+      if (to[e] >= 0 && from[e] >= 0) v[e] = base[static_cast<size_t>(from[e]) * step];
+#pragma unroll
+    for (int e = 0; e < kDepth; ++e)
+      if (to[e] >= 0 && from[e] >= 0) base[static_cast<size_t>(to[e]) * step] = v[e];
+  }
+  if (p.token_scales)
+    for (int i = w * 32 + lane; i < moves; i += nw * 32) {
+      const int to = holes[i].x, from = movers[i].x;
+      if (to >= 0 && from >= 0)
+        p.token_scales[static_cast<size_t>(to) * p.H + h] = p.token_scales[static_cast<size_t>(from) * p.H + h];
+    }
+}
+
+// SMALL: every CTA has at most kEvSmall slots and keeps their scores and positions.
+template <int T, bool SMALL>
+__global__ void __launch_bounds__(T, 1024 / T) evict_kernel(const EvictParams p) {
+  constexpr int W = T / 32;  // warps
+  // keys [cap] (SMALL: first the scores), SMALL: positions [cap], one word of kept slots per 32
+  extern __shared__ uint32_t dyn[];
+  __shared__ EvictShared<T> sh;
+  uint32_t* kept = dyn + (SMALL ? 2 : 1) * p.cap;
+  int* own_pos = reinterpret_cast<int*>(dyn + p.cap);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = p.cluster, rank = C > 1 ? cluster_rank() : 0;
   const int pair = blockIdx.x / C, s = pair / p.H, h = pair - s * p.H;
@@ -133,226 +222,355 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictParams p) 
   const size_t row = static_cast<size_t>(pair) * p.stride;
   const float* sc = p.scores_in + row;
   const int32_t* po = p.pos_in ? p.pos_in + row : nullptr;
+  float* sc_out = p.scores_out + row;
+  int32_t* po_out = p.pos_out + row;
+  const int32_t* table = p.block_tables + static_cast<size_t>(s) * p.max_blocks;
 
   // this CTA's run of slots [a, b), this warp's [wa, wb), both multiples of 32 long but at the end
   const int per = ((n + C - 1) / C + 31) & ~31, a = min(n, rank * per), b = min(n, a + per);
-  const int wper = ((per + kEvWarps - 1) / kEvWarps + 31) & ~31;
+  const int wper = ((per + W - 1) / W + 31) & ~31;
   const int wa = min(b, a + warp * wper), wb = min(b, wa + wper);
 
-  // ---- 1. the newest position ----
+  // Scores and positions of slots below the new length, unless in place; holes among them are written
+  // again in step 6.
+  const bool sc_apart = sc_out != sc, po_apart = po_out != po;
+  auto copy_out = [&](int j, float x, int pos) {
+    if (j >= left) return;
+    if (sc_apart) sc_out[j] = x;
+    if (po_apart) po_out[j] = pos;
+  };
+
+  // ---- 1. the newest position (and, SMALL, the slots' scores and positions) ----
   int newest = n - 1;
-  if (po) {
+  if (SMALL || po) {
     int mx = -1;
 #pragma unroll 4
-    for (int j = wa + lane; j < wb; j += 32) mx = max(mx, po[j]);
-    mx = __reduce_max_sync(0xffffffffu, mx);
-    if (tid == 0) sh_max = -1;
-    __syncthreads();
-    if (lane == 0) atomicMax(&sh_max, mx);
-    cluster_sync_all(C);
-    newest = sh_max;
-    for (int c = 0; c < C && C > 1; ++c) newest = max(newest, remote_ld(&sh_max, c));
+    for (int j = wa + lane; j < wb; j += 32) {
+      const int x = po ? po[j] : j;
+      if constexpr (SMALL) {
+        const float y = sc[j];
+        dyn[j - a] = __float_as_uint(y);
+        own_pos[j - a] = x;
+        copy_out(j, y, x);
+      }
+      mx = max(mx, x);
+    }
+    if (po) {
+      mx = __reduce_max_sync(0xffffffffu, mx);
+      if (tid == 0) sh.max = -1;
+      __syncthreads();
+      if (lane == 0) atomicMax(&sh.max, mx);
+      cluster_sync_all(C);
+      newest = sh.max;
+      for (int c = 0; c < C && C > 1; ++c) newest = max(newest, remote_ld(&sh.max, c));
+    }
   }
-  const long long recent_from = static_cast<long long>(newest) - p.recent;  // positions past it are recent
+  const int recent_from = newest - p.recent;  // positions past it are recent (newest >= -1: no overflow)
 
-  auto make_key = [&](int j) -> uint32_t {
-    const int pos = po ? po[j] : j;
-    return (pos < p.anchors || pos > recent_from) ? 0xFFFFFFFFu : score_key(sc[j]);
+  auto key_of = [&](float x, int pos) -> uint32_t {
+    return (pos < p.anchors || pos > recent_from) ? 0xFFFFFFFFu : score_key(x);
   };
-  auto key = [&](int j) -> uint32_t { return j - a < p.key_cap ? keys[j - a] : make_key(j); };
+  const bool full = SMALL || per <= p.cap;  // every key of this CTA is in shared memory
+  auto key = [&](int j) -> uint32_t {
+    return full || j - a < p.cap ? dyn[j - a] : key_of(sc[j], po ? po[j] : j);
+  };
 
   uint32_t thr = 0;  // keys above it are kept, `need` of those equal to it too
-  int need = n, eq_base = 0;
-  bool rank_eq = false;
+  int need = n, moves = 0;
   if (n > p.budget) {
-    // ---- 2. keys ----
-#pragma unroll 4
-    for (int j = wa + lane; j < wb; j += 32)
-      if (j - a < p.key_cap) keys[j - a] = make_key(j);
-
-    // ---- 3. the budget-th largest key ----
+    // ---- 2, 3. the budget-th largest key ----
     uint32_t mask = 0;
     int rest = p.budget;
+    bool listed = false;  // sh.list holds this CTA's keys that share the digits so far
     for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
-      for (int i = tid; i < kEvBins; i += kEvThreads) hist[i] = 0;
+      const int shift = pass == 0 ? 20 : (pass == 1 ? 10 : 0), bits = pass == 0 ? 12 : 10;
+      const int bins = 1 << bits;
+      for (int i = tid; i < kEvRun * kEvPitch / 4; i += T) reinterpret_cast<int4*>(sh.hist)[i] = make_int4(0, 0, 0, 0);
+      if (tid < kEvRuns) sh.runs[tid] = 0;
+      if (tid == 0) sh.run = -1;
       __syncthreads();
-      for (int j0 = wa; j0 < wb; j0 += 32) {
-        const int j = j0 + lane;
-        const uint32_t k = j < wb ? key(j) : 0u;
-        const bool in = j < wb && (k & mask) == thr;
-        const uint32_t d = (k >> shift) & ((1u << bits) - 1u);
-        // a warp whose keys share the digit adds once (scores that are all zero, or protected slots)
-        const unsigned who = __ballot_sync(0xffffffffu, in);
-        if (who == 0) continue;
-        const uint32_t d0 = __shfl_sync(0xffffffffu, d, __ffs(who) - 1);
-        if (__all_sync(0xffffffffu, !in || d == d0)) {
-          if (lane == 0) atomicAdd(&hist[d0], __popc(who));
+      auto count = [&](bool in, uint32_t k) {  // every lane of the warp takes part
+        const uint32_t d = (k >> shift) & static_cast<uint32_t>(bins - 1);
+        // a warp whose keys share the digit adds once (scores that are all zero, recent slots)
+        const uint32_t d0 = __shfl_sync(0xffffffffu, d, 0);
+        if (__all_sync(0xffffffffu, in && d == d0)) {
+          if (lane == 0) atomicAdd(&sh.hist[bin_at(d)], 32);
         } else if (in) {
-          atomicAdd(&hist[d], 1);
+          atomicAdd(&sh.hist[bin_at(d)], 1);
+        }
+      };
+      if (pass == 0) {
+        constexpr int kAhead = SMALL ? 2 : 8;  // slots per lane that are loaded together
+        for (int g0 = wa; g0 < wb; g0 += 32 * kAhead) {
+          uint32_t k[kAhead];
+          float x[kAhead];
+          int pos[kAhead];
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+            const int j = g0 + 32 * i + lane;
+            x[i] = j >= wb ? 0.f : (SMALL ? __uint_as_float(dyn[j - a]) : sc[j]);
+            pos[i] = j >= wb ? 0 : (SMALL ? own_pos[j - a] : (po ? po[j] : j));
+          }
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+            const int j = g0 + 32 * i + lane;
+            k[i] = key_of(x[i], pos[i]);
+            if (!SMALL && j < wb) copy_out(j, x[i], pos[i]);
+          }
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+            const int j = g0 + 32 * i + lane;
+            if (j < wb && (full || j - a < p.cap)) dyn[j - a] = k[i];
+            count(j < wb, k[i]);
+          }
+        }
+      } else if (listed) {
+        for (int i0 = warp * 32; i0 < sh.listed; i0 += T) {
+          const uint32_t k = i0 + lane < sh.listed ? sh.list[i0 + lane] : 0u;
+          count(i0 + lane < sh.listed && (k & mask) == thr, k);
+        }
+      } else {
+        for (int j0 = wa; j0 < wb; j0 += 32) {
+          const uint32_t k = j0 + lane < wb ? key(j0 + lane) : 0u;
+          count(j0 + lane < wb && (k & mask) == thr, k);
         }
       }
       cluster_sync_all(C);
-      // thread i sums bins 4i .. 4i + 3 over the cluster, then the bins above them over the CTA
-      int cnt[4];
+      // this CTA's share of the runs of bins, nt of them, summed over the cluster: one thread per (CTA, run)
+      const int nt = bins / kEvRun / C, first_run = rank * nt;
+      int mine = 0, above, own;
+      if (tid < nt * C) {
+        const int c = tid / nt, run = tid - c * nt;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        cnt[e] = 0;
-        if (C > 1) {
-          for (int c = 0; c < C; ++c) cnt[e] += remote_ld(&hist[4 * tid + e], c);
-        } else {
-          cnt[e] = hist[4 * tid + e];
+        for (int e = 0; e < kEvRun; ++e) {
+          const int* at = &sh.hist[e * kEvPitch + first_run + run];
+          mine += C > 1 ? remote_ld(at, c) : *at;
         }
+        if (C > 1) atomicAdd(&sh.runs[run], mine);
       }
-      const int mine = cnt[0] + cnt[1] + cnt[2] + cnt[3];
+      if (C > 1) {
+        __syncthreads();
+        mine = tid < nt ? sh.runs[tid] : 0;
+      }
       int suffix = mine;  // over this thread and the lanes above it
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
         const int v = __shfl_down_sync(0xffffffffu, suffix, off);
         if (lane + off < 32) suffix += v;
       }
-      if (lane == 0) above_warp[warp] = suffix;
+      if (lane == 0) sh.above_warp[warp] = suffix;
+      if (tid == 0 && pass == 0) sh.listed = 0;
       __syncthreads();
-      int above = suffix - mine;
-      for (int w = warp + 1; w < kEvWarps; ++w) above += above_warp[w];
+      own = warps_sum<W>(sh.above_warp, &above, true);
+      above += suffix - mine;
+      if (C > 1) {  // the shares above this CTA's
+        if (tid < C) remote_st(&sh.slice[rank], tid, own);
+        cluster_sync_all(C);
+        for (int c = rank + 1; c < C; ++c) above += sh.slice[c];
+      }
+      if (above < rest && rest <= above + mine) {  // one thread of the cluster: the rest-th largest is in its run
+        sh.run = first_run + tid;
+        sh.above = above;
+      }
+      __syncthreads();
+      if (warp == 0 && sh.run >= 0) {  // its bin: one lane each
+        int cnt = 0;
+        if (lane < kEvRun)
+          for (int c = 0; c < C; ++c) {
+            const int* at = &sh.hist[lane * kEvPitch + sh.run];
+            cnt += C > 1 ? remote_ld(at, c) : *at;
+          }
+        int up = cnt;
 #pragma unroll
-      for (int e = 3; e >= 0; --e) {  // exactly one bin holds the rest-th largest
-        if (above < rest && rest <= above + cnt[e]) {
-          sh_digit = 4 * tid + e;
-          sh_rest = rest - above;
-          sh_count = cnt[e];
+        for (int off = 1; off < kEvRun; off <<= 1) {
+          const int v = __shfl_down_sync(0xffffffffu, up, off);
+          if (lane + off < 32) up += v;
         }
-        above += cnt[e];
+        up += sh.above - cnt;  // keys in the bins above
+        if (up < rest && rest <= up + cnt) {
+          for (int c = 0; c < C; ++c) {
+            if (C > 1) {
+              remote_st(&sh.digit, c, sh.run * kEvRun + lane);
+              remote_st(&sh.rest, c, rest - up);
+              remote_st(&sh.count, c, cnt);
+            } else {
+              sh.digit = sh.run * kEvRun + lane;
+              sh.rest = rest - up;
+              sh.count = cnt;
+            }
+          }
+        }
       }
       cluster_sync_all(C);  // the digit is known, and no CTA still reads another's histogram
-      thr |= static_cast<uint32_t>(sh_digit) << shift;
-      mask |= ((1u << bits) - 1u) << shift;
-      rest = sh_rest;
+      const int own_count = sh.hist[bin_at(sh.digit)];  // this CTA's keys that share it
+      thr |= static_cast<uint32_t>(sh.digit) << shift;
+      mask |= static_cast<uint32_t>(bins - 1) << shift;
+      rest = sh.rest;
+      if (pass == 0 && own_count <= kEvList) {
+        listed = true;
+        for (int g0 = wa; g0 < wb; g0 += 128) {
+          uint32_t k[4], m[4];
+          int all = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = g0 + 32 * i + lane;
+            k[i] = j < wb ? key(j) : 0u;
+            m[i] = __ballot_sync(0xffffffffu, j < wb && (k[i] & mask) == thr);
+            all += __popc(m[i]);
+          }
+          if (all == 0) continue;
+          int at = lane == 0 ? atomicAdd(&sh.listed, all) : 0;
+          at = __shfl_sync(0xffffffffu, at, 0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if ((m[i] >> lane) & 1u) sh.list[at + __popc(m[i] & low_bits(lane))] = k[i];
+            at += __popc(m[i]);
+          }
+        }
+      }
+      __syncthreads();  // the list is complete, and the histogram may be cleared
     }
     need = rest;
-    rank_eq = sh_count > need;
 
-    // ---- 4. ranks of the slots equal to the threshold, when not all of them stay ----
-    if (rank_eq) {
-      int cnt = 0, all;
+    // ---- 4. the kept slots ----
+    uint32_t* words = kept + ((wa - a) >> 5);
+    if (sh.count == need) {  // every slot equal to the threshold stays
+      for (int g0 = wa; g0 < wb; g0 += 128) {
+        uint32_t m[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = g0 + 32 * i + lane;
+          m[i] = __ballot_sync(0xffffffffu, j < wb && key(j) >= thr);
+        }
+        if (lane < 4 && g0 + 32 * lane < wb)
+          words[((g0 - wa) >> 5) + lane] = lane == 0 ? m[0] : (lane == 1 ? m[1] : (lane == 2 ? m[2] : m[3]));
+      }
+    } else {
+      int cnt[1] = {0}, before[1], all[1];
       for (int j0 = wa; j0 < wb; j0 += 32) {
         const int j = j0 + lane;
-        cnt += __popc(__ballot_sync(0xffffffffu, j < wb && key(j) == thr));
+        cnt[0] += __popc(__ballot_sync(0xffffffffu, j < wb && key(j) == thr));
       }
-      eq_base = warp_prefix(cnt, sh_warp[0], &sh_tot[0], warp, lane, rank, C, &all);
+      warp_prefix<T, 1>(sh, 0, cnt, before, all, rank, C);
+      int eq = before[0];  // slots equal to the threshold so far
+      for (int j0 = wa; j0 < wb; j0 += 32) {
+        const int j = j0 + lane;
+        const uint32_t k = j < wb ? key(j) : 0u;
+        const bool same = j < wb && k == thr;
+        const uint32_t em = __ballot_sync(0xffffffffu, same);
+        const uint32_t m = __ballot_sync(
+            0xffffffffu, j < wb && (k > thr || (same && eq + __popc(em & low_bits(lane)) < need)));
+        if (lane == 0) words[(j0 - wa) >> 5] = m;
+        eq += __popc(em);
+      }
     }
-  }
+    __syncwarp();
 
-  // ---- 5. holes and movers ----
-  const unsigned below = (1u << lane) - 1u;
-  int moves = 0, hole_base = 0, mover_base = 0;
-  // kept slots of 32 at j0; `eq` counts the slots equal to the threshold before them
-  auto keep_at = [&](int j0, int& eq) -> bool {
-    const int j = j0 + lane;
-    if (n <= p.budget) return j < wb;
-    const uint32_t k = j < wb ? key(j) : 0u;
-    const unsigned same = __ballot_sync(0xffffffffu, j < wb && k == thr);
-    const bool keep = j < wb && (k > thr || (k == thr && (!rank_eq || eq + __popc(same & below) < need)));
-    eq += __popc(same);
-    return keep;
-  };
-  if (n > p.budget) {
-    int hc = 0, mc = 0, eq = eq_base, all;
-    for (int j0 = wa; j0 < wb; j0 += 32) {
-      const bool keep = keep_at(j0, eq);
-      const int j = j0 + lane;
-      hc += __popc(__ballot_sync(0xffffffffu, j < wb && j < left && !keep));
-      mc += __popc(__ballot_sync(0xffffffffu, j >= left && keep));
+    // ---- 5. holes and movers: counted, then ranked and listed, one lane per word ----
+    const int nw = (wb - wa + 31) >> 5;
+    int cnt[2] = {0, 0}, before[2], all[2];
+    for (int i = lane; i < nw; i += 32) {
+      const int j0 = wa + 32 * i;
+      const uint32_t m = words[i], under = low_bits(left - j0);
+      cnt[0] += __popc(low_bits(wb - j0) & under & ~m);
+      cnt[1] += __popc(m & ~under);
     }
-    hole_base = warp_prefix(hc, sh_warp[1], &sh_tot[1], warp, lane, rank, C, &moves);
-    mover_base = warp_prefix(mc, sh_warp[2], &sh_tot[2], warp, lane, rank, C, &all);
-  }
-  auto physical = [&](int j) -> int {
-    const int e = p.block_tables[static_cast<size_t>(s) * p.max_blocks + j / PA_BLOCK_SIZE];
-    if (e < 0 || e >= p.num_blocks) {
-      set_error(p.err, PA_EFLAG_BAD_BLOCK_ID);
-      return -1;
-    }
-    return e * PA_BLOCK_SIZE + j % PA_BLOCK_SIZE;
-  };
-  int2* holes = p.holes + static_cast<size_t>(pair) * p.max_moves;
-  int4* movers = p.movers + static_cast<size_t>(pair) * p.max_moves;
-  {
-    int eq = eq_base;
-    for (int j0 = wa; j0 < wb; j0 += 32) {
-      const bool keep = keep_at(j0, eq);
-      const int j = j0 + lane;
-      const bool hole = j < wb && j < left && !keep, mover = j >= left && keep;
-      const unsigned hm = __ballot_sync(0xffffffffu, hole), mm = __ballot_sync(0xffffffffu, mover);
-      if (j < wb) {
-        const float x = sc[j];
-        const int pos = po ? po[j] : j;
-        if (hole) holes[hole_base + __popc(hm & below)] = make_int2(physical(j), j);
-        if (mover) movers[mover_base + __popc(mm & below)] = make_int4(physical(j), __float_as_int(x), pos, 0);
-        if (j >= left) {
-          p.scores_out[row + j] = 0.f;
-          p.pos_out[row + j] = newest + 1 + (j - left);
-        } else if (keep) {
-          p.scores_out[row + j] = x;
-          p.pos_out[row + j] = pos;
-        }
+    cnt[0] = __reduce_add_sync(0xffffffffu, cnt[0]);
+    cnt[1] = __reduce_add_sync(0xffffffffu, cnt[1]);
+    warp_prefix<T, 2>(sh, 1, cnt, before, all, rank, C);
+    moves = all[0];
+    int2* holes = p.holes + static_cast<size_t>(pair) * p.max_moves;
+    int2* movers = p.movers + static_cast<size_t>(pair) * p.max_moves;
+    for (int i0 = 0; i0 < nw; i0 += 32) {
+      const int j0 = wa + 32 * (i0 + lane);
+      uint32_t hm = 0u, mm = 0u;
+      if (i0 + lane < nw) {
+        const uint32_t m = words[i0 + lane], under = low_bits(left - j0);
+        hm = low_bits(wb - j0) & under & ~m;
+        mm = m & ~under;
       }
-      hole_base += __popc(hm);
-      mover_base += __popc(mm);
+      const int both = __popc(hm) | (__popc(mm) << 16);  // up to 1024 each over the warp
+      int incl = both;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += v;
+      }
+      const int sum = __shfl_sync(0xffffffffu, incl, 31);
+      // the word's two blocks: first slot in the pool, or a negative number for an entry outside it
+      int first[2] = {-64, -64};
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        if (((hm | mm) >> (16 * q)) & 0xFFFFu) {
+          const int e = table[j0 / PA_BLOCK_SIZE + q];
+          if (e >= 0 && e < p.num_blocks) first[q] = e * PA_BLOCK_SIZE;
+          else set_error(p.err, PA_EFLAG_BAD_BLOCK_ID);
+        }
+      for (int i = 0; i < min(32, nw - i0); ++i) {
+        const uint32_t hw = __shfl_sync(0xffffffffu, hm, i), mw = __shfl_sync(0xffffffffu, mm, i);
+        const int at = __shfl_sync(0xffffffffu, incl - both, i);
+        const int f0 = __shfl_sync(0xffffffffu, first[0], i), f1 = __shfl_sync(0xffffffffu, first[1], i);
+        const int2 entry = make_int2((lane < 16 ? f0 : f1) + (lane & 15), wa + 32 * (i0 + i) + lane);
+        if ((hw >> lane) & 1u) holes[before[0] + (at & 0xFFFF) + __popc(hw & low_bits(lane))] = entry;
+        if ((mw >> lane) & 1u) movers[before[1] + (at >> 16) + __popc(mw & low_bits(lane))] = entry;
+      }
+      before[0] += sum & 0xFFFF;
+      before[1] += sum >> 16;
     }
   }
-  for (int j = n + rank * kEvThreads + tid; j < p.stride; j += C * kEvThreads) {
-    p.scores_out[row + j] = 0.f;
-    p.pos_out[row + j] = newest + 1 + (j - left);
-  }
+  if (!SMALL && n <= p.budget)  // (else copied as the keys were made)
+    for (int j = wa + lane; j < wb; j += 32) copy_out(j, sc[j], po ? po[j] : j);
+  // Past the new length: at once when no mover is still to be read there.
+  auto clear = [&] {
+    for (int j = left + rank * T + tid; j < p.stride; j += C * T) {
+      sc_out[j] = 0.f;
+      po_out[j] = newest + 1 + (j - left);
+    }
+  };
+  if (sc_apart && po_apart) clear();
 
   // ---- 6. move ----
-  __threadfence();
   // every list entry of this (sequence, head) is written, and no CTA still reads another's shared memory
+  __threadfence();
   cluster_sync_all(C);
-  if (n <= p.budget) return;
-  for (int i = rank * kEvThreads + tid; i < moves; i += C * kEvThreads) {
-    const int2 d = holes[i];
-    const int4 m = movers[i];
-    p.scores_out[row + d.y] = __int_as_float(m.y);
-    p.pos_out[row + d.y] = m.z;
-    if (p.token_scales && d.x >= 0 && m.x >= 0)
-      p.token_scales[static_cast<size_t>(d.x) * p.H + h] = p.token_scales[static_cast<size_t>(m.x) * p.H + h];
+  const int2* holes = p.holes + static_cast<size_t>(pair) * p.max_moves;
+  const int2* movers = p.movers + static_cast<size_t>(pair) * p.max_moves;
+  for (int i = rank * T + tid; i < moves; i += C * T) {
+    const int to = holes[i].y, from = movers[i].y;
+    sc_out[to] = sc[from];
+    po_out[to] = po ? po[from] : from;
   }
-  const long long all_units = static_cast<long long>(moves) * p.total_units;
-  constexpr int kDepth = 4;  // loads in flight per thread
-  for (long long u0 = static_cast<long long>(rank) * kEvThreads + tid; u0 < all_units;
-       u0 += static_cast<long long>(C) * kEvThreads * kDepth) {
-    uint4 v[kDepth];
-    uint4* dst[kDepth];
-#pragma unroll
-    for (int e = 0; e < kDepth; ++e) {
-      const long long u = u0 + static_cast<long long>(e) * C * kEvThreads;
-      dst[e] = nullptr;
-      if (u < all_units) {
-        const int i = static_cast<int>(u / p.total_units);
-        int r = static_cast<int>(u - static_cast<long long>(i) * p.total_units), t = 0;
-        while (r >= p.units[t]) r -= p.units[t++];
-        const int to = holes[i].x, from = movers[i].x;
-        if (to >= 0 && from >= 0) {
-          dst[e] = p.part[t] + (static_cast<size_t>(to) * p.H + h) * p.units[t] + r;
-          v[e] = p.part[t][(static_cast<size_t>(from) * p.H + h) * p.units[t] + r];
-        }
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < kDepth; ++e)
-      if (dst[e]) *dst[e] = v[e];
+  if constexpr (SMALL) {
+    move_rows(p, pair, moves, rank * W + warp, C * W);
+  } else if (rank == 0 && tid == 0) {
+    p.counts[pair] = moves;
   }
+  if (!(sc_apart && po_apart)) {
+    cluster_sync_all(C);  // in place, the movers' scores have been read before they are cleared
+    clear();
+  }
+}
+
+// The second launch: blockIdx.x of gridDim.x shares of the rows of (sequence, head) blockIdx.y.
+__global__ void __launch_bounds__(256) evict_rows_kernel(const EvictParams p) {
+  const int warp = threadIdx.x >> 5, share = blockIdx.x, shares = gridDim.x;
+  const int pair = blockIdx.y + 65535 * blockIdx.z;
+  if (pair >= p.B * p.H) return;
+  grid_dep_wait();
+  const int n = p.context_lens[pair / p.H];  // (a context out of range has no count)
+  if (n <= p.budget || n > p.max_ctx || static_cast<long long>(n) > static_cast<long long>(p.max_blocks) * PA_BLOCK_SIZE)
+    return;
+  move_rows(p, pair, min(p.counts[pair], p.max_moves), share * 8 + warp, shares * 8);
 }
 
 int evict_max_moves(int max_ctx, int budget) { return std::max(0, std::min(budget, max_ctx - budget)); }
 
 bool evict_layout(const pa_cache_desc* d, int max_ctx, int budget, size_t* movers_off, size_t* total) {
-  if (validate_desc(d) != PA_OK || max_ctx < 0 || max_ctx > 0x7FFFFF00 || budget < 1) return false;
-  const size_t rows = static_cast<size_t>(d->num_seqs) * d->num_kv_heads * evict_max_moves(max_ctx, budget);
+  if (validate_desc(d) != PA_OK || max_ctx < 0 || budget < 1) return false;
+  const size_t pairs = static_cast<size_t>(d->num_seqs) * d->num_kv_heads;
+  const size_t rows = pairs * evict_max_moves(max_ctx, budget);
   *movers_off = (rows * sizeof(int2) + 255) / 256 * 256;
-  *total = *movers_off + rows * sizeof(int4) + 256;
+  *total = 2 * *movers_off + (pairs * sizeof(int) + 255) / 256 * 256 + 256;
   return true;
 }
 
@@ -374,6 +592,7 @@ extern "C" pa_status pa_cache_evict(const pa_cache_desc* desc, void* k_cache, vo
   if (desc->sliding_window > 0) return PA_ERR_UNSUPPORTED;  // a window counts slots in order of position
   size_t movers_off = 0, total = 0;
   if (!pa::evict_layout(desc, max_context_len, budget, &movers_off, &total)) return PA_ERR_INVALID_ARG;
+  if (max_context_len > pa::kEvMaxContext) return PA_ERR_UNSUPPORTED;
   if (stride < max_context_len || num_recent < 0 || num_anchor < desc->num_sink ||
       static_cast<long long>(num_anchor) + num_recent > budget)
     return PA_ERR_INVALID_ARG;
@@ -405,7 +624,8 @@ extern "C" pa_status pa_cache_evict(const pa_cache_desc* desc, void* k_cache, vo
   p.pos_out = pos_out;
   p.max_moves = pa::evict_max_moves(max_context_len, budget);
   p.holes = static_cast<int2*>(workspace);
-  p.movers = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + movers_off);
+  p.movers = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + movers_off);
+  p.counts = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + 2 * movers_off);
   p.err = err_flag;
   const bool int4 = pa::is_int4(desc);
   const int row16 = static_cast<int>((int4 ? pa::int4_code_row_bytes(desc)
@@ -422,19 +642,29 @@ extern "C" pa_status pa_cache_evict(const pa_cache_desc* desc, void* k_cache, vo
   if (pa::has_token_scales(desc))
     p.token_scales = reinterpret_cast<float*>(static_cast<uint8_t*>(k_cache) + pa::token_scales_offset(desc));
 
-  // CTAs per (sequence, head): enough that each has a few thousand slots
+  // CTAs per (sequence, head): more while all of them stay resident at once (four of 256 threads on an
+  // SM) and each has 1024 slots or more, or while one has more than its shared memory takes.  Measured:
+  // 512 pairs of 2112 slots take 25 us with one CTA and 46 with two, 128 pairs of up to 8192 slots 51, 47,
+  // 38 and 57 us with one, two, four and eight.
+  const long long pairs = static_cast<long long>(p.B) * p.H, resident = 4LL * std::max(1, pa::sm_count_current());
   int C = 1;
-  while (C < pa::kEvMaxCluster && (max_context_len + C - 1) / C > PA_EVICT_SPAN) C *= 2;
-  const long long pairs = static_cast<long long>(p.B) * p.H;
+  while (C < pa::kEvMaxCluster && (max_context_len / C > 32768 ||
+                                   (max_context_len / (2 * C) >= 1024 && pairs * 2 * C <= resident)))
+    C *= 2;
+#ifdef PA_EVICT_CLUSTER
+  C = PA_EVICT_CLUSTER;
+#endif
   if (pairs * C > 0x7FFFFFFFLL) return PA_ERR_UNSUPPORTED;
   p.cluster = C;
-  const size_t span = (static_cast<size_t>((max_context_len + C - 1) / C) + 31) / 32 * 32;
-  const size_t key_bytes = std::min(pa::kEvMaxKeyBytes, std::max<size_t>(span, 32) * 4);
-  p.key_cap = static_cast<int>(key_bytes / 4);
-  if (!pa::ensure_dynamic_smem(reinterpret_cast<const void*>(pa::evict_kernel), key_bytes)) return PA_ERR_CUDA;
+  const size_t span = std::max<size_t>((static_cast<size_t>((max_context_len + C - 1) / C) + 31) / 32 * 32, 32);
+  const bool small = span <= static_cast<size_t>(pa::kEvSmall);
+  p.cap = static_cast<int>(small ? span : std::min<size_t>(span, pa::kEvMaxKeys));
+  const size_t key_bytes = static_cast<size_t>(p.cap) * (small ? 8 : 4) + span / 8;
+  auto kern = small ? pa::evict_kernel<256, true> : pa::evict_kernel<512, false>;
+  if (!pa::ensure_dynamic_smem(reinterpret_cast<const void*>(kern), key_bytes)) return PA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(pairs * C));
-  cfg.blockDim = dim3(pa::kEvThreads);
+  cfg.blockDim = dim3(small ? 256 : 512);
   cfg.dynamicSmemBytes = key_bytes;
   cfg.stream = pa::as_stream(stream);
   cudaLaunchAttribute attr[2];
@@ -446,5 +676,12 @@ extern "C" pa_status pa_cache_evict(const pa_cache_desc* desc, void* k_cache, vo
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, pa::evict_kernel, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return PA_ERR_CUDA;
+  if (small || p.max_moves == 0) return PA_OK;
+  // the rows: eight CTAs per SM in all, none with less than a round of its warps' rows
+  const long long round = 8LL * 4 * (32 / p.total_units);
+  const long long shares = std::max(1LL, std::min(2 * resident / pairs, (p.max_moves + round - 1) / round));
+  const dim3 rows(static_cast<unsigned>(shares), static_cast<unsigned>(std::min(pairs, 65535LL)),
+                  static_cast<unsigned>((pairs + 65534) / 65535));
+  return pa::launch_overlapped(pa::evict_rows_kernel, rows, dim3(256), 0, pa::as_stream(stream), p);
 }

@@ -135,10 +135,11 @@ def test_weights():
 @host_only
 def test_evict():
     d = _desc(sliding_window=0)
-    # at most min(budget, context - budget) rows move per (sequence, KV head): 8 and 16 bytes each
+    # at most min(budget, context - budget) rows move per (sequence, KV head), 8 bytes for either end of
+    # each, and a count per (sequence, KV head)
     for max_ctx, budget, rows in ((1000, 900, 100), (1000, 300, 300), (1000, 1000, 0), (0, 5, 0)):
         a = (64 * rows * 8 + 255) // 256 * 256
-        assert N.pa_cache_evict_workspace_size(d, max_ctx, budget) == a + 64 * rows * 16 + 256
+        assert N.pa_cache_evict_workspace_size(d, max_ctx, budget) == 2 * a + 256 + 256
     assert N.pa_cache_evict_workspace_size(d, 1000, 0) == 0 and N.pa_cache_evict_workspace_size(d, -1, 5) == 0
     need = N.pa_cache_evict_workspace_size(d, 1000, 900)
 
@@ -153,6 +154,7 @@ def test_evict():
              dict(desc=_desc(sliding_window=0, num_sink=5, k_sink=FAKE, v_sink=FAKE))]  # anchors below the sinks
     _refused(call, {}, [(kw, N.PA_ERR_INVALID_ARG) for kw in inval] + [
         (dict(n=need - 1), N.PA_ERR_WORKSPACE_TOO_SMALL), (dict(desc=_desc()), N.PA_ERR_UNSUPPORTED),
+        (dict(max_ctx=2 ** 21 + 1, stride=2 ** 22), N.PA_ERR_UNSUPPORTED),
         (dict(desc=_desc(sliding_window=0, head_dim=96)), N.PA_ERR_UNSUPPORTED)])
     call(desc=_desc(sliding_window=0, num_seqs=0))
 
