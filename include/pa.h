@@ -306,8 +306,7 @@ pa_status pa_decode_attention_anchored(const pa_cache_desc* desc, void* out, con
  *                 of two.  The size is 0 when an argument is invalid.
  * A query head whose softmax has no sum (no position, or NaN scores: its output row is zero) adds
  * nothing.  Every cache kind; other arguments, device errors and host errors as pa_decode_attention;
- * PA_ERR_UNSUPPORTED when num_kv_heads * ceil(max_context_len / 1024) passes what one launch takes
- * (about 65000). */
+ * PA_ERR_UNSUPPORTED for more than 5000 query heads. */
 size_t pa_decode_weights_workspace_size(const pa_cache_desc* desc, int max_context_len, int partition_size);
 
 pa_status pa_decode_attention_weights(const pa_cache_desc* desc, void* out, const void* q,

@@ -478,7 +478,7 @@ struct Consumer {
 
   // Online-softmax update over NB blocks' scores at once (one maximum, one rescale check);
   // pr[b] = this lane's unnormalised probabilities {row t4: head 2tq, 2tq+1; row t4+8: same}.
-  // raw[b]: where the scores of block b's first token go (WT).
+  // raw[b]: where this lane's scores of block b go (WT).
   template <int NB>
   __device__ __forceinline__ void softmax_n(const float (&acc)[NB][4], const int (&first)[NB], const int (&ntok)[NB],
                                             float (&pr)[NB][4], float* const (&raw)[NB]) {
@@ -493,14 +493,16 @@ struct Consumer {
       s[b][2] = v1 ? acc[b][2] * sl[0] : kNegInf;
       s[b][3] = v1 ? acc[b][3] * sl[1] : kNegInf;
       if constexpr (WT) {
-        // 16 tokens x raw_g heads: a quad's lanes write consecutive heads of one token
-        if (p.raw_g == 1) {
-          if (tq == 0 && v0) raw[b][t4] = s[b][0];
-          if (tq == 0 && v1) raw[b][t4 + 8] = s[b][2];
-        } else if (2 * tq < p.raw_g) {
-          float2* r = reinterpret_cast<float2*>(raw[b] + t4 * p.raw_g + 2 * tq);
-          if (v0) r[0] = make_float2(s[b][0], s[b][1]);
-          if (v1) r[4 * p.raw_g] = make_float2(s[b][2], s[b][3]);
+        // 16 tokens x raw_g heads: a quad's lanes write consecutive heads of one token (raw[b] is this
+        // lane's place for token t4, or null for a lane whose heads do not exist)
+        if (raw[b]) {
+          if (p.raw_g == 1) {
+            if (v0) raw[b][0] = s[b][0];
+            if (v1) raw[b][8] = s[b][2];
+          } else {
+            if (v0) *reinterpret_cast<float2*>(raw[b]) = make_float2(s[b][0], s[b][1]);
+            if (v1) *reinterpret_cast<float2*>(raw[b] + 8 * p.raw_g) = make_float2(s[b][2], s[b][3]);
+          }
         }
       }
       bm0 = fmaxf(bm0, fmaxf(s[b][0], s[b][2]));
@@ -626,7 +628,7 @@ struct Consumer {
   // one maximum and one rescale check for both, then both P·V products.
   __device__ __forceinline__ void block2(const uint8_t* s0, int f0, int n0, const uint8_t* s1, int f1, int n1,
                                          float* raw0) {
-    float* const raw[2] = {raw0, WT ? raw0 + PA_BLOCK_SIZE * p.raw_g : raw0};  // consecutive logical blocks
+    float* const raw[2] = {raw0, WT && raw0 ? raw0 + PA_BLOCK_SIZE * p.raw_g : raw0};  // consecutive logical blocks
     float acc[2][4], pr[2][4];
     const int f[2] = {f0, f1}, n[2] = {n0, n1};
     if constexpr (I4) {
@@ -997,6 +999,7 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1)
   auto covers = [&](int s_rel) -> bool { return sm.cum[s_rel] >= u0 && sm.cum[s_rel + 1] <= u1; };
   int cur = s_first;
   bool q_loaded = false;
+  float* raw_seq = nullptr;  // WT: this lane's place for list entry 0 of the current sequence
   for (int k = 0; k < n_iters; ++k) {
     const int st = k % S;
     const uint32_t ph = static_cast<uint32_t>(k / S) & 1u;
@@ -1018,15 +1021,20 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1)
       if (!q_loaded) {
         c.load_q(seq_base + cur);
         q_loaded = true;
+        if constexpr (WT) {
+          const int col = p.raw_g == 1 ? c.tq : 2 * c.tq;  // this lane's (first) query head
+          raw_seq = col >= p.raw_g ? nullptr
+                                   : p.raw + ((static_cast<size_t>(seq_base + cur) * p.H_kv + c.h_kv) * p.raw_ctx +
+                                              sm.los[cur] / PA_BLOCK_SIZE * PA_BLOCK_SIZE + c.t4) * p.raw_g + col;
+        }
       }
       if (mt.w) {
         c.bad = true;
       } else {
         const uint8_t* stage = sm.stages + static_cast<size_t>(st) * p.stage_bytes;
         float* raw = nullptr;
-        if constexpr (WT)
-          raw = p.raw + ((static_cast<size_t>(seq_base + cur) * p.H_kv + c.h_kv) * p.raw_ctx +
-                         Producer<KIND>::logical(p, sm, cur, u) * PA_BLOCK_SIZE) * p.raw_g;
+        if constexpr (WT)  // (no anchors here: the list is one run of blocks)
+          raw = raw_seq ? raw_seq + static_cast<ptrdiff_t>(u - sm.cum[cur]) * (PA_BLOCK_SIZE * p.raw_g) : nullptr;
         if constexpr (MAXW <= 8) {
           // one block per stage: take the next stage too when its block belongs to the same
           // sequence, and run both as one 32-token step (every warp decides alike: the
@@ -1243,27 +1251,31 @@ __global__ void __launch_bounds__(128) merge_kernel(const DecodeParams p, int gr
 // ------------------------------------------------------------------------------------
 // Accumulated attention weights: scores_out[s][h_kv][t] = scores_in[s][h_kv][t] + sum over the G query
 // heads of 2^(x_t - M) / L, x_t the stored scores, M and L the row's maximum and sum over all of its
-// partials and sinks.  Positions outside the attended range keep their score.  A CTA takes `chunk`
-// positions of one (sequence, KV head) and works M and L of its G rows out for itself: a few (m, l)
-// pairs each, all L2 hits.  It runs beside the merge's CTAs in one launch, as both need nothing but
-// the decode kernel.
+// partials and sinks.  Positions outside the attended range keep their score.  A CTA takes a share of
+// one (sequence, KV head)'s positions, chunks of 128 P of them, and works M and L of its G rows out for
+// itself: a few (m, l) pairs each, all L2 hits, but three dependent round trips, so that there are no
+// more shares than keep the SMs busy.  It runs beside the merge's CTAs in one launch, as both need
+// nothing but the decode kernel.
 // ------------------------------------------------------------------------------------
 struct WeightsParams {
   const float* scores_in;  // or null: zeros
   float* scores_out;
   int stride;   // scores of one (sequence, KV head) row
-  int chunk;    // positions per CTA
   int merge_y;  // grid.y of the merge part
-  int chunks;   // CTAs per (sequence, KV head)
+  int shares;   // CTAs per (sequence, KV head)
 };
 
-template <int D>
-__device__ __forceinline__ void weights_rows(const DecodeParams& p, const WeightsParams& wp, int grid_x, int h_kv,
-                                             int c0) {
-  constexpr int E = D / 32;
+// GP: p.raw_g.  A thread takes positions c0 + tid + 128 i of a chunk; the first chunk's scores are loaded
+// before M and L are known, so that the loads run beside the partials'.
+constexpr int weights_per_thread(int gp) { return gp == 8 ? 4 : 8; }
+
+template <int D, int GP>
+__device__ __forceinline__ void weights_rows(const DecodeParams& p, const WeightsParams& wp, int grid_x, int y) {
+  constexpr int E = D / 32, P = weights_per_thread(GP), CHUNK = 128 * P;
   __shared__ float sh_m[8], sh_inv[8];
   __shared__ int sh_bad;
   const int s = blockIdx.x, tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
+  const int h_kv = y / wp.shares, share = y - h_kv * wp.shares;
   if (tid == 0) sh_bad = 0;
   grid_dep_wait();
   int cs = 0, ce = 0, T = 0;
@@ -1274,8 +1286,36 @@ __device__ __forceinline__ void weights_rows(const DecodeParams& p, const Weight
   }
   const int ctx = p.context_lens[s];
   const int nb = seq_span(p, s, ctx);
+  int c0 = share * CHUNK;
   if (nb < 0 || c0 >= ctx) return;
-  const int lo = seq_lo(p, s, ctx), n_sink = min(p.num_sink, ctx);
+  const int lo = seq_lo(p, s, ctx), n_sink = min(p.num_sink, ctx), first = max(lo, n_sink);
+  float* raw = p.raw + (static_cast<size_t>(s) * p.H_kv + h_kv) * p.raw_ctx * GP;
+  const size_t row = (static_cast<size_t>(s) * p.H_kv + h_kv) * wp.stride;
+  auto load = [&](int t, float (&x)[GP]) {
+    const float* at = raw + static_cast<size_t>(t) * GP;
+    if constexpr (GP >= 4) {
+#pragma unroll
+      for (int g = 0; g < GP; g += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(at + g);
+        x[g] = v.x, x[g + 1] = v.y, x[g + 2] = v.z, x[g + 3] = v.w;
+      }
+    } else if constexpr (GP == 2) {
+      const float2 v = *reinterpret_cast<const float2*>(at);
+      x[0] = v.x, x[1] = v.y;
+    } else {
+      x[0] = *at;
+    }
+  };
+  float x[P][GP], base[P];
+  auto load_chunk = [&] {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int t = c0 + tid + 128 * i;
+      base[i] = t < ctx && wp.scores_in ? wp.scores_in[row + t] : 0.f;
+      if (t < ctx && t >= first) load(t, x[i]);
+    }
+  };
+  load_chunk();
   int c_first = 0, c_last = -1;
   if (nb > 0) {
     if (p.mode == 0) {
@@ -1287,7 +1327,6 @@ __device__ __forceinline__ void weights_rows(const DecodeParams& p, const Weight
     }
   }
   const int n_parts = (c_last - c_first + 1) * p.nbs;
-  float* raw = p.raw + (static_cast<size_t>(s) * p.H_kv + h_kv) * p.raw_ctx * p.raw_g;
   __syncthreads();
   for (int g = wid; g < p.G; g += 4) {  // one warp per query head: M and L
     const int h = h_kv * p.G + g;
@@ -1325,7 +1364,7 @@ __device__ __forceinline__ void weights_rows(const DecodeParams& p, const Weight
 #pragma unroll
         for (int mask = 1; mask < 32; mask <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, mask);
         const float st = dot * p.scale_log2;
-        if (lane == 0 && t >= c0 && t < c0 + wp.chunk) raw[static_cast<size_t>(t) * p.raw_g + g] = st;
+        if (lane == 0 && t / CHUNK % wp.shares == share) raw[static_cast<size_t>(t) * GP + g] = st;
         const float mn = fmaxf(Mw, st);
         Lw = (Lw != 0.f ? Lw * ex2(Mw - mn) : 0.f) + ex2(st - mn);
         Mw = mn;
@@ -1339,39 +1378,39 @@ __device__ __forceinline__ void weights_rows(const DecodeParams& p, const Weight
   }
   __syncthreads();
   if (sh_bad) return;  // a table entry outside the pool: the row of scores is left as it was
-  const size_t row = (static_cast<size_t>(s) * p.H_kv + h_kv) * wp.stride;
-  const int end = min(ctx, c0 + wp.chunk);
-  auto weight = [&](float x, int g) {  // a score of NaN, or a row without a sum, adds nothing
-    const float e = ex2(x - sh_m[g]) * sh_inv[g];
-    return e > 0.f ? e : 0.f;
-  };
-#pragma unroll 4
-  for (int t = c0 + tid; t < end; t += 128) {
-    const float base = wp.scores_in ? wp.scores_in[row + t] : 0.f;
-    float w = 0.f;
-    if (t >= lo) {
-      const float* x = raw + static_cast<size_t>(t) * p.raw_g;
-      if (p.raw_g >= 4) {
-        for (int g = 0; g < p.G; g += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(x + g);
-          const float xs[4] = {v.x, v.y, v.z, v.w};
+  float m[GP], inv[GP];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (g + e < p.G) w += weight(xs[e], g + e);
+  for (int g = 0; g < GP; ++g) {
+    m[g] = g < p.G ? sh_m[g] : 0.f;
+    inv[g] = g < p.G ? sh_inv[g] : 0.f;
+  }
+  while (true) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int t = c0 + tid + 128 * i;
+      if (t >= ctx) break;
+      float w = 0.f;
+      if (t >= lo) {
+        if (t < n_sink) load(t, x[i]);
+#pragma unroll
+        for (int g = 0; g < GP; ++g) {  // a score of NaN, a row without a sum and the padding add nothing
+          const float e = ex2(x[i][g] - m[g]) * inv[g];
+          w += e > 0.f ? e : 0.f;
         }
-      } else {
-        for (int g = 0; g < p.G; ++g) w += weight(x[g], g);
       }
+      wp.scores_out[row + t] = base[i] + w;  // (the step's weights summed first: one rounding into the score)
     }
-    wp.scores_out[row + t] = base + w;  // (the step's weights summed first: one rounding into the score)
+    if (ctx - c0 <= wp.shares * CHUNK) break;
+    c0 += wp.shares * CHUNK;
+    load_chunk();
   }
 }
 
-template <int D, int WPR>
+template <int D, int WPR, int GP>
 __global__ void __launch_bounds__(128) merge_weights_kernel(const DecodeParams p, const WeightsParams wp, int grid_x) {
   const int y = static_cast<int>(blockIdx.y) - wp.merge_y;
   if (y < 0) merge_rows<D, WPR, 8>(p, grid_x);
-  else weights_rows<D>(p, wp, grid_x, y / wp.chunks, (y % wp.chunks) * wp.chunk);
+  else weights_rows<D, GP>(p, wp, grid_x, y);
 }
 
 // ------------------------------------------------------------------------------------
@@ -1460,8 +1499,31 @@ pa_status make_plan(const pa_cache_desc* d, int max_ctx, int partition_size, Pla
   return PA_OK;
 }
 
-// positions of one CTA of the weights part
-constexpr int kWeightsChunk = 1024;
+// CTAs of the weights part per SM
+#ifndef PA_WEIGHTS_CTAS
+#define PA_WEIGHTS_CTAS 4
+#endif
+
+template <int D, int WPR, int GP>
+pa_status launch_weights_tail(const Plan& pl, const DecodeParams& p, WeightsParams wp, cudaStream_t stream) {
+  constexpr int chunk = 128 * weights_per_thread(GP);
+  const long long pairs = static_cast<long long>(p.B) * p.H_kv, chunks = (p.max_ctx + chunk - 1) / chunk;
+  const long long want = (PA_WEIGHTS_CTAS * static_cast<long long>(std::max(1, sm_count_current())) + pairs - 1) / pairs;
+  wp.shares = static_cast<int>(std::max(1LL, std::min({chunks, want, 60000LL / p.H_kv})));
+  const long long ny = wp.merge_y + static_cast<long long>(p.H_kv) * wp.shares;
+  return launch_overlapped(merge_weights_kernel<D, WPR, GP>, dim3(p.B, static_cast<unsigned>(ny)), dim3(128), 0, stream,
+                           p, wp, pl.grid_x);
+}
+
+template <int D, int WPR>
+pa_status launch_weights_tail(const Plan& pl, const DecodeParams& p, const WeightsParams& wp, cudaStream_t stream) {
+  switch (p.raw_g) {
+    case 1: return launch_weights_tail<D, WPR, 1>(pl, p, wp, stream);
+    case 2: return launch_weights_tail<D, WPR, 2>(pl, p, wp, stream);
+    case 4: return launch_weights_tail<D, WPR, 4>(pl, p, wp, stream);
+    default: return launch_weights_tail<D, WPR, 8>(pl, p, wp, stream);
+  }
+}
 
 template <int D, int KIND>
 pa_status launch_weights(const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mkp,
@@ -1475,15 +1537,9 @@ pa_status launch_weights(const Plan& pl, const CUtensorMap& mk, const CUtensorMa
   const dim3 grid = p.mode == 0 ? dim3(pl.grid_x, pl.n_hg, 1) : dim3(pl.max_parts, p.B, pl.n_hg);
   if (launch_overlapped(kern, grid, dim3(pl.threads), pl.smem_bytes, stream, mk, mv, mkp, mvp, p) != PA_OK)
     return PA_ERR_CUDA;
-  wp.chunk = kWeightsChunk;
-  wp.chunks = std::max(1, (p.max_ctx + wp.chunk - 1) / wp.chunk);
   const bool few = static_cast<long long>(p.B) * p.H_q < 4LL * std::max(1, sm_count_current());
   wp.merge_y = few ? p.H_q : (p.H_q + 3) / 4;
-  const long long ny = wp.merge_y + static_cast<long long>(p.H_kv) * wp.chunks;
-  if (ny > 65535) return PA_ERR_UNSUPPORTED;
-  const dim3 tail(p.B, static_cast<unsigned>(ny));
-  if (few) return launch_overlapped(merge_weights_kernel<D, 4>, tail, dim3(128), 0, stream, p, wp, pl.grid_x);
-  return launch_overlapped(merge_weights_kernel<D, 1>, tail, dim3(128), 0, stream, p, wp, pl.grid_x);
+  return few ? launch_weights_tail<D, 4>(pl, p, wp, stream) : launch_weights_tail<D, 1>(pl, p, wp, stream);
 }
 
 template <int D, int KIND>
@@ -1742,6 +1798,7 @@ extern "C" pa_status pa_decode_attention_weights(const pa_cache_desc* desc, void
   size_t raw_off = 0, total = 0;
   if (!pa::weights_layout(desc, max_context_len, partition_size, &raw_off, &total)) return PA_ERR_INVALID_ARG;
   if (score_stride < max_context_len) return PA_ERR_INVALID_ARG;
+  if (desc->num_q_heads > 5000) return PA_ERR_UNSUPPORTED;  // grid.y of the tail
   if (desc->num_seqs == 0) return PA_OK;
   if (!scores_out || !workspace || ((reinterpret_cast<uintptr_t>(scores_in) | reinterpret_cast<uintptr_t>(scores_out)) & 3u))
     return PA_ERR_INVALID_ARG;
