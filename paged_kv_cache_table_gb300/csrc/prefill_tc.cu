@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const bool row_ok = tq0 + tok < it.t_end;
       const int row_pos = it.first_pos + tq0 + tok;
       const int row_lo = p.window > 0 ? max(0, row_pos - p.window + 1) : 0;
-      const int fcols = ANCH ? it.ab * PA_BLOCK_SIZE : 0;  // list columns of the anchors' own blocks
+      const int kbase0 = (it.kb0 - (ANCH ? it.ab : 0)) * PA_BLOCK_SIZE;  // position of list column 0, window part
       float m_run = kNegInfTc, l_run = 0.f;
       for (int k = 0; ok && k < nt; ++k) {
         if (!warp_wait(&s_full[wg], sp & 1u)) {
@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * c));
         tmem_wait_ld();
-        const int kbase = (it.kb0 - (ANCH ? it.ab : 0) + 8 * k) * PA_BLOCK_SIZE;
+        const int kbase = kbase0 + 128 * k;
         // scores stay raw (the scale is positive, so the maximum commutes with it); only tiles
         // that cross a row's causal or window edge take the per-key mask, and within them only
         // the 32-key chunks that some row of the warp attends in part (a row attends the tile's
@@ -679,36 +679,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // the keys past the item's last query on its diagonal tile) takes no maximum and no
         // exponentials: its P is zero.
         unsigned dead = 0;
-        if constexpr (ANCH) {
-          // columns [0, an) are anchors, [lo, hi] the row's window; one interval when they meet
-          int lo = row_lo - kbase, an = row_ok ? p.anchors - 128 * k : 0;
-          const int hi = row_ok ? row_pos - kbase : -1;
-          if (an >= lo) lo = an = 0;
-          if (!__all_sync(0xffffffffu, lo <= 0 && hi >= 127)) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if (__all_sync(0xffffffffu, (lo <= 32 * q && hi >= 32 * q + 31) || an >= 32 * q + 32)) continue;
-              if (__all_sync(0xffffffffu, (hi < 32 * q || lo > 32 * q + 31) && an <= 32 * q)) {
-                dead |= 1u << q;
-                continue;
-              }
-#pragma unroll
-              for (int c = 32 * q; c < 32 * q + 32; ++c)
-                if ((c < lo || c > hi) && c >= an) sv[c] = __float_as_uint(kNegInfTc);
-            }
-          }
-        } else if (!__all_sync(0xffffffffu, row_ok && kbase + 127 <= row_pos && kbase >= row_lo)) {
+        if (!__all_sync(0xffffffffu, row_ok && kbase + 127 <= row_pos && kbase >= row_lo)) {
           const int lo = row_lo - kbase, hi = row_ok ? row_pos - kbase : -1;
+          const int an = ANCH ? p.anchors - 128 * k : 0;  // columns below it are anchors, attended up to hi
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            if (__all_sync(0xffffffffu, lo <= 32 * q && hi >= 32 * q + 31)) continue;
-            if (__all_sync(0xffffffffu, hi < 32 * q || lo > 32 * q + 31)) {
+            if (__all_sync(0xffffffffu, hi >= 32 * q + 31 && (lo <= 32 * q || an >= 32 * q + 32))) continue;
+            if (__all_sync(0xffffffffu, hi < 32 * q || (lo > 32 * q + 31 && an <= 32 * q))) {
               dead |= 1u << q;
               continue;
             }
 #pragma unroll
             for (int c = 32 * q; c < 32 * q + 32; ++c)
-              if (c < lo || c > hi) sv[c] = __float_as_uint(kNegInfTc);
+              if (c > hi || (c < lo && !(ANCH && c < an))) sv[c] = __float_as_uint(kNegInfTc);
           }
         }
         float mx4[4] = {kNegInfTc, kNegInfTc, kNegInfTc, kNegInfTc};
@@ -728,8 +711,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         m_run = m_new;
         // key row r of V: zero it when it holds no loaded in-context data (both groups write the
         // same zeros; each must see them before its own P·V)
-        const int kp_r = ANCH && 128 * k + r < fcols ? 128 * k + r : kbase + r;
-        const bool zero_row = (kp_r < it.kv_lo && !(ANCH && kp_r < p.anchors)) || kp_r >= it.loaded_end;
+        const int kp_r = kbase + r;
+        const bool zero_row = (kp_r < it.kv_lo && !(ANCH && 128 * k + r < p.anchors)) || kp_r >= it.loaded_end;
         const int gk = g + k, vs = gk % kVStages;
         if (__any_sync(0xffffffffu, zero_row)) {
           // the stage's copies must have landed first
