@@ -1076,6 +1076,29 @@ __global__ void __launch_bounds__((MAXW + 1) * 32, 1)
 // combined through shared memory by the same log-sum-exp rule.  CH partials are loaded per
 // round: 8, or 16 when a shared prefix adds its rows (one round for both kinds).
 // ------------------------------------------------------------------------------------
+// A lane's E (2 or 4) dims of a bf16 sink row.
+template <int E>
+struct SinkRow {
+  uint32_t w[E / 2];
+  __device__ __forceinline__ void load(const __nv_bfloat16* at) {
+    if ((reinterpret_cast<uintptr_t>(at) & (2 * E - 1)) != 0) {  // a buffer of any alignment is taken
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) {
+        const uint16_t* h = reinterpret_cast<const uint16_t*>(at) + 2 * i;
+        w[i] = h[0] | static_cast<uint32_t>(h[1]) << 16;
+      }
+    } else if constexpr (E == 4) {
+      const uint2 x = *reinterpret_cast<const uint2*>(at);
+      w[0] = x.x, w[1] = x.y;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(at);
+    }
+  }
+  __device__ __forceinline__ float at(int e) const {
+    return __uint_as_float((e & 1) ? (w[e >> 1] & 0xFFFF0000u) : (w[e >> 1] << 16));
+  }
+};
+
 template <int D, int WPR, int CH>
 __device__ __forceinline__ void merge_rows(const DecodeParams& p, int grid_x) {
   constexpr int E = D / 32;  // dims per lane
@@ -1192,21 +1215,37 @@ __device__ __forceinline__ void merge_rows(const DecodeParams& p, int grid_x) {
   }
   bad = __any_sync(0xffffffffu, bad);
 
-  // bf16 sink tokens join the merge as single-token partials: the anchors among them, then the window's
-  for (int t = sink_a > 0 ? 0 : sink_lo; t < n_sink; t = t + 1 == sink_a ? sink_lo : t + 1) {
-    const size_t off = ((static_cast<size_t>(s) * p.num_sink + t) * p.H_kv + h_kv) * D + lane * E;
-    float dot = 0.f;
+  // bf16 sink tokens join the merge as single-token partials: the anchors among them, then the window's;
+  // four tokens' rows are loaded together.
+  for (int t = sink_a > 0 ? 0 : sink_lo; t < n_sink;) {
+    int ts[4];
+    SinkRow<E> k[4], v[4];
 #pragma unroll
-    for (int e = 0; e < E; ++e) dot += qv[e] * __bfloat162float(p.k_sink[off + e]);
+    for (int i = 0; i < 4; ++i) {
+      ts[i] = t;
+      if (t < n_sink) {
+        const size_t off = ((static_cast<size_t>(s) * p.num_sink + t) * p.H_kv + h_kv) * D + lane * E;
+        k[i].load(p.k_sink + off);
+        v[i].load(p.v_sink + off);
+        t = t + 1 == sink_a ? sink_lo : t + 1;
+      }
+    }
 #pragma unroll
-    for (int mask = 1; mask < 32; mask <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, mask);
-    const float st = dot * p.scale_log2;
-    const float newM = fmaxf(M, st);
-    const float sc = ex2(M - newM), w = ex2(st - newM);
-    L = L * sc + w;
+    for (int i = 0; i < 4; ++i) {
+      if (ts[i] >= n_sink) break;
+      float dot = 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * sc + w * __bfloat162float(p.v_sink[off + e]);
-    M = newM;
+      for (int e = 0; e < E; ++e) dot += qv[e] * k[i].at(e);
+#pragma unroll
+      for (int mask = 1; mask < 32; mask <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, mask);
+      const float st = dot * p.scale_log2;
+      const float newM = fmaxf(M, st);
+      const float sc = ex2(M - newM), w = ex2(st - newM);
+      L = L * sc + w;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = acc[e] * sc + w * v[i].at(e);
+      M = newM;
+    }
   }
   if constexpr (WPR > 1) {
     // the warps' (M, L, acc) -> one row: weights e^{M_w - max M}, warps without a partial weigh 0
@@ -1356,11 +1395,15 @@ __device__ __forceinline__ void weights_rows(const DecodeParams& p, const Weight
       float qv[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) qv[e] = __bfloat162float(qrow[e]);
+      SinkRow<E> k;
+      const __nv_bfloat16* krow = p.k_sink + (static_cast<size_t>(s) * p.num_sink * p.H_kv + h_kv) * D + lane * E;
+      k.load(krow + static_cast<size_t>(lo) * p.H_kv * D);
       for (int t = lo; t < n_sink; ++t) {
-        const __nv_bfloat16* krow = p.k_sink + ((static_cast<size_t>(s) * p.num_sink + t) * p.H_kv + h_kv) * D + lane * E;
+        const SinkRow<E> kt = k;
+        if (t + 1 < n_sink) k.load(krow + static_cast<size_t>(t + 1) * p.H_kv * D);
         float dot = 0.f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) dot += qv[e] * __bfloat162float(krow[e]);
+        for (int e = 0; e < E; ++e) dot += qv[e] * kt.at(e);
 #pragma unroll
         for (int mask = 1; mask < 32; mask <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, mask);
         const float st = dot * p.scale_log2;

@@ -648,6 +648,9 @@ pa_status prefill_check(const pa_cache_desc* desc, const void* out, const void* 
   if ((reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache) |
        reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15u)
     return PA_ERR_INVALID_ARG;
+  // sink rows are read 16 bytes at a time
+  if (desc->num_sink > 0 && ((reinterpret_cast<uintptr_t>(desc->k_sink) | reinterpret_cast<uintptr_t>(desc->v_sink)) & 15u))
+    return PA_ERR_INVALID_ARG;
   if (desc->num_seqs > 65535 || desc->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
   *work = true;
   return PA_OK;

@@ -102,6 +102,8 @@ def test_anchored_prefill():
         (dict(scale=-0.1), N.PA_ERR_INVALID_ARG), (dict(scale=float("nan")), N.PA_ERR_INVALID_ARG),
         (dict(ws=0), N.PA_ERR_INVALID_ARG), (dict(ws=FAKE + 16), N.PA_ERR_INVALID_ARG),
         (dict(n=need - 1), N.PA_ERR_WORKSPACE_TOO_SMALL)])
+    odd = _desc(num_sink=4, k_sink=FAKE + 8, v_sink=FAKE, **QUANT)
+    _refused(call, dict(desc=odd, n=1 << 40), [(dict(), N.PA_ERR_INVALID_ARG)])  # sink rows are read 16 bytes at a time
     call(desc=_desc(num_seqs=0, **QUANT))
     call(max_q=0)
 

@@ -92,6 +92,22 @@ def test_decode_window_reaching_the_sinks(sinks, anchors):
     _decode_loop(w, 45, anchors, 32)
 
 
+@pytest.mark.parametrize("offset", [1, 2, 4])
+def test_decode_sink_buffers_of_any_alignment(offset):
+    w = workload("fp8", sinks=5, ctx_list=[2, 19, 47, 150, 333])
+    g, o = states(w, 45)
+    ctx = w.ctx_old
+    want = decode_anchored(g, w.q[0], ctx, 5)
+    for name in ("k_sink", "v_sink"):
+        old = getattr(g, name)
+        flat = torch.empty(old.numel() + 8, dtype=old.dtype, device="cuda")[offset:offset + old.numel()]
+        flat.copy_(old.view(-1))
+        setattr(g, name, flat)
+        setattr(g.desc, name, flat.data_ptr())
+    assert torch.equal(decode_anchored(g, w.q[0], ctx, 5).view(torch.int16), want.view(torch.int16))
+    assert g.err_bits() == 0
+
+
 def test_decode_without_anchors_is_the_window_bit_for_bit():
     w = workload("bf16", ctx_list=[0, 30, 80, 150, 333])
     g, _ = states(w, 45)
