@@ -419,7 +419,9 @@ pa_status pa_prefill_step_ws(const pa_cache_desc* desc, void* out, const void* q
  *                     pa_prefill_attention_ws, but only the blocks that the chunk can attend, so its
  *                     size goes with W + max_query_len + num_anchor, not with the context.  The size
  *                     is 0 when the call needs none (as pa_prefill_workspace_size; workspace may then
- *                     be NULL) or an argument is invalid.
+ *                     be NULL) or an argument is invalid.  With anchors and a window, 8-bit caches with
+ *                     per-head scales keep their bare codes there (the scales multiply the scores and
+ *                     the output), so that K and V are not rounded; other decoded values are, to bf16.
  * A sequence that breaks pa_prefill_attention's rules, or (with a workspace) has a context beyond
  * max_context_len, sets PA_EFLAG_CTX_OVERFLOW and gets zero rows; other rules, device errors and
  * host errors as pa_prefill_attention_ws. */

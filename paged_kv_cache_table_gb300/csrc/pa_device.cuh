@@ -229,6 +229,10 @@ __device__ __forceinline__ uint32_t nib_pair(uint32_t w, int i) {
   return ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
 }
 
+// What a per-head scale contributes when K or V are kept divided by it: the scale itself, or 1 (the
+// values then carry it) for one that a score cannot be scaled by after its maximum was taken.
+__device__ __forceinline__ float folded_scale(float x) { return x > 0.f && x < 3.0e38f ? x : 1.f; }
+
 __device__ __forceinline__ float warp_max_xor(float v, int mask) {
   return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, mask));
 }

@@ -79,10 +79,13 @@ bool ensure_dynamic_smem(const void* kernel, size_t bytes);
 // step: the previous kernel on the stream is the append of this prefill step (it writes only
 // K/V slots), so only the K/V copies wait for it.
 // anchors: positions below it stay visible beside the sliding window (0: none).
+// k_scales, v_scales (anchors > 0 and a window only): K and V hold values divided by these scales per KV
+// head (folded_scale of each), which the kernel applies to the scores and the output.
 pa_status launch_prefill_tc(const pa_cache_desc* desc, void* out, const void* q, const void* k_cache,
                             const void* v_cache, const int32_t* block_tables, const int32_t* q_start,
                             const int32_t* context_lens, int max_query_len, float scale, int32_t* err_flag,
-                            cudaStream_t stream, bool step, int anchors = 0);
+                            cudaStream_t stream, bool step, int anchors = 0, const float* k_scales = nullptr,
+                            const float* v_scales = nullptr);
 
 // Shared-prefix decode (shared_prefix.cu).  Per-sequence flags, zeroed then or-ed by the prefix
 // kernel: kSharedMember = listed, in range, context covering the prefix; kSharedMismatch = some

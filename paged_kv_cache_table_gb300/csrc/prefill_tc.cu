@@ -95,6 +95,10 @@ constexpr uint32_t kIdescPV = kIdescS | (1u << 16);
 struct TcParams {
   int B, H_q, H_kv, G, num_blocks, max_blocks, max_q, window;
   int anchors;  // positions below it stay visible beside the window (ANCH)
+  // FOLD, K and V of an 8-bit cache as bare codes: their scales per KV head, which multiply the scores
+  // and the output (as folded_scale of each)
+  const float* k_scales;
+  const float* v_scales;
   int tpq;  // tokens per query tile: 128 / G (a CTA holds two tiles)
   int step;  // the previous kernel is this step's append: only the K/V copies wait for it
   float scale_log2;
@@ -297,7 +301,8 @@ __device__ __forceinline__ Item make_item(const TcParams& p, const ItemRec& e) {
 // on the same CTA.
 __device__ __forceinline__ int round_pos(int r, int NC, int cid) { return r * NC + ((r & 1) ? NC - 1 - cid : cid); }
 
-template <bool ANCH>
+// ANCH: with anchors.  FOLD (with ANCH): k_scales and v_scales apply.
+template <bool ANCH, bool FOLD>
 __global__ void __launch_bounds__(kTcThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
@@ -317,7 +322,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* o_done = bars + 18;  // [2]
   uint64_t* drain = bars + 20;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 21);
-  int* flags = reinterpret_cast<int*>(bars + 22);  // [0] tiles of all sequences, [1] a wait gave up
+  int* flags = reinterpret_cast<int*>(bars + 22);  // [0] tiles of all sequences, [1] a wait gave up, [2..3] score scales
   ItemRec* list = reinterpret_cast<ItemRec*>(sm + kListOff);  // this CTA's items, in order
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -659,6 +664,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int row_lo = p.window > 0 ? max(0, row_pos - p.window + 1) : 0;
       const int kbase0 = (it.kb0 - (ANCH ? it.ab : 0)) * PA_BLOCK_SIZE;  // position of list column 0, window part
       float m_run = kNegInfTc, l_run = 0.f;
+      // FOLD: the score scale of this KV head goes through shared memory, read again at each use: held in a
+      // register across the tile loop it costs the loop twice its time (the scores take 128 of 168)
+      volatile float* head_scale = reinterpret_cast<volatile float*>(flags + 2) + wg;
+      if constexpr (FOLD) {
+        if (r == 0) *head_scale = p.scale_log2 * folded_scale(p.k_scales[it.h_kv]);
+        group_sync(1 + wg);  // (its readers of the item before have met at that item's output)
+      }
       for (int k = 0; ok && k < nt; ++k) {
         if (!warp_wait(&s_full[wg], sp & 1u)) {
           ok = false;
@@ -703,7 +715,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mx4[(c >> 1) & 3] = max3f(mx4[(c >> 1) & 3], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
         }
         const float mraw = fmaxf(max3f(mx4[0], mx4[1], mx4[2]), mx4[3]);
-        const float mx = mraw == kNegInfTc ? kNegInfTc : mraw * p.scale_log2;
+        const float mx = mraw == kNegInfTc ? kNegInfTc : mraw * (FOLD ? *head_scale : p.scale_log2);
         const float m_new = (m_run == kNegInfTc || mx > m_run + 8.f) ? fmaxf(m_run, mx) : m_run;
         const float ms = m_new == kNegInfTc ? 0.f : m_new;
         const float alpha = ex2(m_run - ms);
@@ -733,7 +745,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // P (bf16 pairs) over the S columns just read: column c holds keys 2c and 2c + 1; when the
         // maximum moved, O is rescaled before P is handed over.
         float ls4[4] = {0.f, 0.f, 0.f, 0.f};
-        const float sl = p.scale_log2;
+        const float sl = FOLD ? *head_scale : p.scale_log2;
 #pragma unroll
         for (int h = 0; h < 4; ++h) {  // a quarter (32 keys, 16 columns) at a time
           uint32_t pw[16];
@@ -792,7 +804,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // zero rows are selected, not multiplied: O may hold NaN when a block was not loaded (its
       // stage keeps earlier bytes) or no key was attended
       const bool zero_out = !ok || bad || !(l_run > 0.f);
-      const float inv = zero_out ? 0.f : 1.f / l_run;
+      const float vs = FOLD ? folded_scale(p.v_scales[it.h_kv]) : 1.f;
+      const float inv = zero_out ? 0.f : vs / l_run;
       const int g_last = g - 1;
       uint8_t* stile =
           wg == 0 ? sm + kKOff + (g_last % kKStages) * kTile : sm + kVOff + (g_last % kVStages) * kTile;
@@ -868,7 +881,7 @@ int resident_ctas() {
   if (dev < 64 && cached[dev] > 0) return cached[dev];
   int sms = 0, per_sm = 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, prefill_tc_kernel<false>, kTcThreads, kTcSmem) != cudaSuccess ||
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, prefill_tc_kernel<false, false>, kTcThreads, kTcSmem) != cudaSuccess ||
       per_sm <= 0) {
     cudaGetLastError();
     per_sm = 1;
@@ -884,7 +897,8 @@ int resident_ctas() {
 pa_status launch_prefill_tc(const pa_cache_desc* desc, void* out, const void* q, const void* k_cache,
                             const void* v_cache, const int32_t* block_tables, const int32_t* q_start,
                             const int32_t* context_lens, int max_query_len, float scale, int32_t* err_flag,
-                            cudaStream_t stream, bool step, int anchors) {
+                            cudaStream_t stream, bool step, int anchors, const float* k_scales,
+                            const float* v_scales) {
   const long long slots = static_cast<long long>(desc->num_blocks) * PA_BLOCK_SIZE;
   CUtensorMap mk, mv, mq, mo;
   const int G = desc->num_q_heads / desc->num_kv_heads;
@@ -903,6 +917,8 @@ pa_status launch_prefill_tc(const pa_cache_desc* desc, void* out, const void* q,
   p.max_q = max_query_len;
   p.window = desc->sliding_window;
   p.anchors = anchors;
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
   p.tpq = 128 / p.G;
   p.step = step ? 1 : 0;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
@@ -912,7 +928,8 @@ pa_status launch_prefill_tc(const pa_cache_desc* desc, void* out, const void* q,
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.out = static_cast<__nv_bfloat16*>(out);
   p.err = err_flag;
-  auto kern = anchors > 0 && p.window > 0 ? prefill_tc_kernel<true> : prefill_tc_kernel<false>;
+  auto kern = prefill_tc_kernel<false, false>;
+  if (anchors > 0 && p.window > 0) kern = k_scales ? prefill_tc_kernel<true, true> : prefill_tc_kernel<true, false>;
   if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kern), kTcSmem)) return PA_ERR_CUDA;
   // Persistent CTAs: as many as run at once, but no more than there are work items, and enough
   // that none holds more than kMaxItems of them.

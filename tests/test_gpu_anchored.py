@@ -240,6 +240,15 @@ def test_prefill_window_reaching_the_sinks(H_q, D, sinks, anchors):
     _prefill_case(w, np.array([1, 2, 1, 3, 1, 1, 20, 30]), 45, anchors)
 
 
+@pytest.mark.parametrize("sinks", [0, 5])
+def test_prefill_scales_of_either_sign(sinks):
+    # a head's scale that is not positive cannot be applied after a row's maximum: it stays with the values
+    w = workload("fp8", sinks=sinks, B=3, ctx_list=[60, 150, 333])
+    w.k_scales[1] *= -1
+    w.v_scales[2] *= -1
+    _prefill_case(w, np.array([20, 1, 70]), 45, 7)
+
+
 def test_prefill_decoded_cache_of_head_dim_64():
     _prefill_case(workload("bf16", sinks=4, H_q=8, H_kv=2, D=64, B=3, ctx_list=[30, 150, 333]),
                   np.array([30, 20, 70]), 45, 21)
