@@ -26,7 +26,7 @@
 //  4. slots equal to it are kept in slot order up to the budget (ranks only when some must go); one word
 //     of kept bits per 32 slots;
 //  5. holes and movers are counted and ranked, one lane per word, and their physical slots go to two lists
-//     in the workspace, one lane per slot (a store of consecutive entries); scores and positions of kept
+//     (in the workspace, or for a CTA alone in shared memory over the keys), one lane per slot (a store of consecutive entries); scores and positions of kept
 //     slots are copied (unless in place);
 //  6. movers' scores and positions go to the holes, and the listed rows move, 16 bytes per lane: a lane's
 //     part of a row (which tensor, which 16 bytes) is the same for every row, and a warp has several rows
@@ -163,10 +163,9 @@ __device__ __forceinline__ void warp_prefix(EvictShared<T>& sh, int q0, const in
 // Rows of the lists of one (sequence, head) that warp `w` of `nw` moves: 16 bytes per lane and row, four
 // rows in flight.  (Loading 32 list entries at once, one per lane, and shuffling them out was slower: 46
 // against 38 us for the 128 pairs of up to 8192 slots.)
-__device__ __forceinline__ void move_rows(const EvictParams& p, int pair, int moves, int w, int nw) {
-  const int lane = threadIdx.x & 31, h = pair % p.H;
-  const int2* holes = p.holes + static_cast<size_t>(pair) * p.max_moves;
-  const int2* movers = p.movers + static_cast<size_t>(pair) * p.max_moves;
+__device__ __forceinline__ void move_rows(const EvictParams& p, int h, const int2* holes, const int2* movers,
+                                          int moves, int w, int nw) {
+  const int lane = threadIdx.x & 31;
   // a lane's 16 bytes of every row it takes: tensor t, unit r of row `sub` of the warp's `group` rows
   const int group = 32 / p.total_units, sub = lane / p.total_units;
   int r = lane - sub * p.total_units, t = 0;
@@ -274,6 +273,15 @@ __global__ void __launch_bounds__(T, 1024 / T) evict_kernel(const EvictParams p)
   auto key = [&](int j) -> uint32_t {
     return full || j - a < p.cap ? dyn[j - a] : key_of(sc[j], po ? po[j] : j);
   };
+
+  // The lists.  A CTA alone keeps them where its keys and positions were (at most n / 2 entries each, and
+  // nothing reads keys or positions after the kept words are known).
+  int2* holes = p.holes + static_cast<size_t>(pair) * p.max_moves;
+  int2* movers = p.movers + static_cast<size_t>(pair) * p.max_moves;
+  if (SMALL && C == 1) {
+    holes = reinterpret_cast<int2*>(dyn);
+    movers = reinterpret_cast<int2*>(own_pos);
+  }
 
   uint32_t thr = 0;  // keys above it are kept, `need` of those equal to it too
   int need = n, moves = 0;
@@ -479,8 +487,6 @@ __global__ void __launch_bounds__(T, 1024 / T) evict_kernel(const EvictParams p)
     cnt[1] = __reduce_add_sync(0xffffffffu, cnt[1]);
     warp_prefix<T, 2>(sh, 1, cnt, before, all, rank, C);
     moves = all[0];
-    int2* holes = p.holes + static_cast<size_t>(pair) * p.max_moves;
-    int2* movers = p.movers + static_cast<size_t>(pair) * p.max_moves;
     for (int i0 = 0; i0 < nw; i0 += 32) {
       const int j0 = wa + 32 * (i0 + lane);
       uint32_t hm = 0u, mm = 0u;
@@ -530,18 +536,16 @@ __global__ void __launch_bounds__(T, 1024 / T) evict_kernel(const EvictParams p)
   if (sc_apart && po_apart) clear();
 
   // ---- 6. move ----
-  // every list entry of this (sequence, head) is written, and no CTA still reads another's shared memory
-  __threadfence();
+  // every list entry of this (sequence, head) is written (the barrier orders the cluster's memory accesses),
+  // and no CTA still reads another's shared memory
   cluster_sync_all(C);
-  const int2* holes = p.holes + static_cast<size_t>(pair) * p.max_moves;
-  const int2* movers = p.movers + static_cast<size_t>(pair) * p.max_moves;
   for (int i = rank * T + tid; i < moves; i += C * T) {
     const int to = holes[i].y, from = movers[i].y;
     sc_out[to] = sc[from];
     po_out[to] = po ? po[from] : from;
   }
   if constexpr (SMALL) {
-    move_rows(p, pair, moves, rank * W + warp, C * W);
+    move_rows(p, h, holes, movers, moves, rank * W + warp, C * W);
   } else if (rank == 0 && tid == 0) {
     p.counts[pair] = moves;
   }
@@ -560,7 +564,9 @@ __global__ void __launch_bounds__(256) evict_rows_kernel(const EvictParams p) {
   const int n = p.context_lens[pair / p.H];  // (a context out of range has no count)
   if (n <= p.budget || n > p.max_ctx || static_cast<long long>(n) > static_cast<long long>(p.max_blocks) * PA_BLOCK_SIZE)
     return;
-  move_rows(p, pair, min(p.counts[pair], p.max_moves), share * 8 + warp, shares * 8);
+  const size_t list = static_cast<size_t>(pair) * p.max_moves;
+  move_rows(p, pair % p.H, p.holes + list, p.movers + list, min(p.counts[pair], p.max_moves), share * 8 + warp,
+            shares * 8);
 }
 
 int evict_max_moves(int max_ctx, int budget) { return std::max(0, std::min(budget, max_ctx - budget)); }
