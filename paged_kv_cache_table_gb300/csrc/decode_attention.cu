@@ -1813,7 +1813,8 @@ namespace {
 bool weights_layout(const pa_cache_desc* desc, int max_context_len, int partition_size, size_t* raw_off,
                     size_t* total) {
   Plan pl;
-  if (make_plan(desc, max_context_len, partition_size, &pl) != PA_OK || max_context_len > 0x7FFFFF00) return false;
+  // (positions are counted past the context by up to a chunk of the tail)
+  if (make_plan(desc, max_context_len, partition_size, &pl) != PA_OK || max_context_len > 0x7FFF0000) return false;
   *raw_off = (pl.ws_bytes + 255) / 256 * 256;
   *total = *raw_off + static_cast<size_t>(desc->num_seqs) * desc->num_kv_heads * raw_positions(max_context_len) *
                           raw_heads(desc->num_q_heads / desc->num_kv_heads) * sizeof(float);

@@ -101,9 +101,10 @@ def test_clusters(n):
     _check(w, [n, 37], n - 1, 0, 1, "ties", given=True)
 
 
-def test_more_slots_than_shared_memory_holds():
-    # eight CTAs of 192 KiB of keys hold 393,216 slots; the rest are ranked from memory
-    n, budget, anchors, recent = 500_001, 70_000, 4, 1000
+@pytest.mark.parametrize("n,budget", [(500_001, 70_000), (1 << 21, 1 << 20)])
+def test_more_slots_than_shared_memory_holds(n, budget):
+    # eight CTAs with 40960 keys each hold 327,680 slots; the rest are ranked from memory
+    anchors, recent = 4, 1000
     blocks = -(-n // 16)
     k = torch.randint(-30000, 30000, (blocks * 16, 1, 64), dtype=torch.int16, device="cuda")
     v = torch.randint(-30000, 30000, (blocks * 16, 1, 64), dtype=torch.int16, device="cuda")
@@ -171,6 +172,44 @@ def test_bad_tables_and_lengths():
     es, ep = oracle_evict(o, [100, 100, 0, 0, 100], sc, None, 112, 40, 4, 10)
     for s in (0, 1, 4):
         assert np.array_equal(so[s].cpu().numpy(), es[s]) and np.array_equal(po[s].cpu().numpy(), ep[s])
+
+
+def test_nothing_cached_and_nothing_to_evict():
+    w = workload("bf16", B=3, H_q=2, H_kv=2, D=64, ctx_list=[0, 5, 40])
+    for lens, max_ctx in (([0, 0, 0], 0), ([0, 5, 40], 40)):
+        g, o = states(w)
+        before = g.k.clone()
+        si = torch.rand(3, 2, 48, device="cuda")
+        so, po = torch.full_like(si, -5.0), torch.full((3, 2, 48), -5, dtype=torch.int32, device="cuda")
+        evict(g, lens, si, so, None, po, 40, 4, 8, max_ctx=max_ctx)
+        assert g.err_bits() == 0
+        es, ep = oracle_evict(o, lens, si.cpu().numpy(), None, 48, 40, 4, 8)
+        assert np.array_equal(so.cpu().numpy(), es) and np.array_equal(po.cpu().numpy(), ep)
+        assert torch.equal(g.k.view(torch.int16), before.view(torch.int16))
+
+
+def test_two_calls_at_once_with_their_own_workspaces():
+    w = workload("bf16", B=2, H_q=2, H_kv=2, D=64, ctx_list=[9000, 5000])
+    runs = []
+    for seed in (1, 2):
+        g, o = states(w)
+        rng = np.random.default_rng(seed)
+        sc = _scores(rng, (2, 2, 9000), "spread")
+        n = N.pa_cache_evict_workspace_size(g.desc, 9000, 1000)
+        runs.append(dict(g=g, o=o, sc=sc, si=torch.from_numpy(sc).cuda(), so=torch.zeros(2, 2, 9000, device="cuda"),
+                         po=torch.zeros(2, 2, 9000, dtype=torch.int32, device="cuda"), ctx=gpu([9000, 5000]), n=n,
+                         ws=torch.empty(n, dtype=torch.uint8, device="cuda"), s=torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for r in runs:
+            N.pa_cache_evict(r["g"].desc, r["g"].k, r["g"].v, r["g"].tables_dev, r["ctx"], 9000, r["si"], r["so"], None,
+                             r["po"], 9000, 1000, 4, 100, r["ws"], r["n"], r["g"].err, r["s"])
+    torch.cuda.synchronize()
+    for r in runs:
+        es, ep = oracle_evict(r["o"], [9000, 5000], r["sc"], None, 9000, 1000, 4, 100)
+        assert np.array_equal(r["so"].cpu().numpy(), es) and np.array_equal(r["po"].cpu().numpy(), ep)
+        assert_pools_equal(r["g"], r["o"])
+        assert r["g"].err_bits() == 0
 
 
 def test_replayed_from_a_graph_on_another_stream():

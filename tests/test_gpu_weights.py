@@ -93,6 +93,44 @@ def test_many_sequences_and_one_long_one():
     _run(workload("bf16", B=2, ctx_list=[3000, 5]))
 
 
+def test_more_sequences_than_the_balanced_split_takes():
+    # over 2048 sequences: fixed partitions, one merge of many short rows
+    w = workload("bf16", B=2100, H_q=2, H_kv=1, D=64, ctx_range=(1, 20))
+    g, o = states(w)
+    scores = torch.full((w.B, 1, 32), -5.0, device="cuda")
+    out = decode_weights(g, w.q[0], w.ctx_old, None, scores)
+    _check(g, o, w.q[0], w.ctx_old, 0, out, np.zeros((w.B, 1, 32)), scores, "2100 sequences", seqs=range(0, w.B, 17))
+    assert g.err_bits() == 0
+
+
+def test_nothing_cached():
+    w = workload("bf16", B=3, ctx_list=[5, 17, 40])
+    g, _ = states(w)
+    scores = torch.full((3, w.H_kv, 8), -5.0, device="cuda")
+    out = decode_weights(g, w.q[0], [0, 0, 0], None, scores, max_ctx=0)
+    assert g.err_bits() == 0
+    assert torch.all(out == 0) and torch.all(scores == -5.0)
+
+
+def test_two_calls_at_once_with_their_own_workspaces():
+    w = workload("fp8", sinks=4, ctx_list=[500, 40, 900, 150, 2600])
+    g, o = states(w)
+    n = N.pa_decode_weights_workspace_size(g.desc, 2600, 0)
+    ctx, q = gpu(w.ctx_old), w.q[0].cuda()
+    runs = [dict(out=torch.zeros((w.B, w.H_q, w.D), dtype=torch.bfloat16, device="cuda"),
+                 sc=torch.full((w.B, w.H_kv, 2600), -5.0, device="cuda"),
+                 ws=torch.empty(n, dtype=torch.uint8, device="cuda"), s=torch.cuda.Stream()) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for r in runs:
+            N.pa_decode_attention_weights(g.desc, r["out"], q, g.k, g.v, g.tables_dev, ctx, 2600, w.scale, 0, None, r["sc"],
+                                          2600, r["ws"], n, g.err, r["s"])
+    torch.cuda.synchronize()
+    for r in runs:
+        _check(g, o, w.q[0], w.ctx_old, 0, r["out"], np.zeros((w.B, w.H_kv, 2600)), r["sc"], "one of two")
+    assert g.err_bits() == 0
+
+
 def test_accumulation_in_place_and_from_nothing():
     w = workload("bf16", ctx_list=[4, 40, 90, 150, 260])
     g, o = states(w)
