@@ -26,12 +26,12 @@
 //  4. slots equal to it are kept in slot order up to the budget (ranks only when some must go); one word
 //     of kept bits per 32 slots;
 //  5. holes and movers are counted and ranked, one lane per word, and their physical slots go to two lists
-//     (in the workspace, or for a CTA alone in shared memory over the keys), one lane per slot (a store of consecutive entries); scores and positions of kept
-//     slots are copied (unless in place);
+//     (in the workspace, or with few slots in shared memory over the keys), one lane per slot, so that a
+//     store writes consecutive entries; scores and positions of kept slots are copied (unless in place);
 //  6. movers' scores and positions go to the holes, and the listed rows move, 16 bytes per lane: a lane's
 //     part of a row (which tensor, which 16 bytes) is the same for every row, and a warp has several rows
-//     in flight.  With many slots per CTA there are few CTAs and many rows, and a second launch with as
-//     many CTAs as the GPU holds moves them.
+//     in flight.  With many slots there are few CTAs and many rows, and a second launch with as many CTAs
+//     as the GPU holds moves them.
 // Everything is integer comparison and counting in a fixed order: the result does not depend on timing.
 
 #include <algorithm>
@@ -199,7 +199,8 @@ __device__ __forceinline__ void move_rows(const EvictParams& p, int h, const int
     }
 }
 
-// SMALL: every CTA has at most kEvSmall slots and keeps their scores and positions.
+// SMALL: one CTA per (sequence, head) with at most kEvSmall slots, which keeps scores and positions in
+// shared memory, and later the lists.
 template <int T, bool SMALL>
 __global__ void __launch_bounds__(T, 1024 / T) evict_kernel(const EvictParams p) {
   constexpr int W = T / 32;  // warps
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(T, 1024 / T) evict_kernel(const EvictParams p)
   uint32_t* kept = dyn + (SMALL ? 2 : 1) * p.cap;
   int* own_pos = reinterpret_cast<int*>(dyn + p.cap);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int C = p.cluster, rank = C > 1 ? cluster_rank() : 0;
+  const int C = SMALL ? 1 : p.cluster, rank = C > 1 ? cluster_rank() : 0;
   const int pair = blockIdx.x / C, s = pair / p.H, h = pair - s * p.H;
   grid_dep_wait();  // the previous kernel of the stream may still be writing any input
   const int n = p.context_lens[s];
@@ -274,14 +275,10 @@ __global__ void __launch_bounds__(T, 1024 / T) evict_kernel(const EvictParams p)
     return full || j - a < p.cap ? dyn[j - a] : key_of(sc[j], po ? po[j] : j);
   };
 
-  // The lists.  A CTA alone keeps them where its keys and positions were (at most n / 2 entries each, and
-  // nothing reads keys or positions after the kept words are known).
-  int2* holes = p.holes + static_cast<size_t>(pair) * p.max_moves;
-  int2* movers = p.movers + static_cast<size_t>(pair) * p.max_moves;
-  if (SMALL && C == 1) {
-    holes = reinterpret_cast<int2*>(dyn);
-    movers = reinterpret_cast<int2*>(own_pos);
-  }
+  // The lists.  SMALL: where the keys and positions were (at most n / 2 entries each, and nothing reads
+  // keys or positions after the kept words are known).
+  int2* holes = SMALL ? reinterpret_cast<int2*>(dyn) : p.holes + static_cast<size_t>(pair) * p.max_moves;
+  int2* movers = SMALL ? reinterpret_cast<int2*>(own_pos) : p.movers + static_cast<size_t>(pair) * p.max_moves;
 
   uint32_t thr = 0;  // keys above it are kept, `need` of those equal to it too
   int need = n, moves = 0;
@@ -545,7 +542,7 @@ __global__ void __launch_bounds__(T, 1024 / T) evict_kernel(const EvictParams p)
     po_out[to] = po ? po[from] : from;
   }
   if constexpr (SMALL) {
-    move_rows(p, h, holes, movers, moves, rank * W + warp, C * W);
+    move_rows(p, h, holes, movers, moves, warp, W);
   } else if (rank == 0 && tid == 0) {
     p.counts[pair] = moves;
   }
@@ -648,14 +645,16 @@ extern "C" pa_status pa_cache_evict(const pa_cache_desc* desc, void* k_cache, vo
   if (pa::has_token_scales(desc))
     p.token_scales = reinterpret_cast<float*>(static_cast<uint8_t*>(k_cache) + pa::token_scales_offset(desc));
 
-  // CTAs per (sequence, head): more while all of them stay resident at once (four of 256 threads on an
-  // SM) and each has 1024 slots or more, or while one has more than its shared memory takes.  Measured:
-  // 512 pairs of 2112 slots take 25 us with one CTA and 46 with two, 128 pairs of up to 8192 slots 51, 47,
-  // 38 and 57 us with one, two, four and eight.
-  const long long pairs = static_cast<long long>(p.B) * p.H, resident = 4LL * std::max(1, pa::sm_count_current());
+  // CTAs per (sequence, head).  A cluster costs about 5 us in barriers, so one CTA takes 16384 slots alone:
+  // 512 pairs of 2112 slots take 22 us with one CTA and 44 with two, 128 of 10000 25 us with one, 30 with
+  // two and 29 with four, 32 of 10000 22, 22 and 20.  Above, a cluster grows to 8192 slots per CTA while the
+  // CTAs about fit the GPU at once (two of 512 threads on an SM): 64 pairs of 32000 take 53, 40, 38 and 45 us
+  // with one, two, four and eight, 128 of them 71, 66, 82 and 99; and while a CTA has more slots than shared
+  // memory holds keys.
+  const long long pairs = static_cast<long long>(p.B) * p.H, sms = std::max(1, pa::sm_count_current());
   int C = 1;
-  while (C < pa::kEvMaxCluster && (max_context_len / C > 32768 ||
-                                   (max_context_len / (2 * C) >= 1024 && pairs * 2 * C <= resident)))
+  while (max_context_len > 16384 && C < pa::kEvMaxCluster && max_context_len / C > 8192 &&
+         (max_context_len / C > pa::kEvMaxKeys || pairs * 2 * C <= sms * 5 / 2))
     C *= 2;
 #ifdef PA_EVICT_CLUSTER
   C = PA_EVICT_CLUSTER;
@@ -663,7 +662,7 @@ extern "C" pa_status pa_cache_evict(const pa_cache_desc* desc, void* k_cache, vo
   if (pairs * C > 0x7FFFFFFFLL) return PA_ERR_UNSUPPORTED;
   p.cluster = C;
   const size_t span = std::max<size_t>((static_cast<size_t>((max_context_len + C - 1) / C) + 31) / 32 * 32, 32);
-  const bool small = span <= static_cast<size_t>(pa::kEvSmall);
+  const bool small = C == 1 && span <= static_cast<size_t>(pa::kEvSmall);
   p.cap = static_cast<int>(small ? span : std::min<size_t>(span, pa::kEvMaxKeys));
   const size_t key_bytes = static_cast<size_t>(p.cap) * (small ? 8 : 4) + span / 8;
   auto kern = small ? pa::evict_kernel<256, true> : pa::evict_kernel<512, false>;
@@ -686,7 +685,7 @@ extern "C" pa_status pa_cache_evict(const pa_cache_desc* desc, void* k_cache, vo
   if (small || p.max_moves == 0) return PA_OK;
   // the rows: eight CTAs per SM in all, none with less than a round of its warps' rows
   const long long round = 8LL * 4 * (32 / p.total_units);
-  const long long shares = std::max(1LL, std::min(2 * resident / pairs, (p.max_moves + round - 1) / round));
+  const long long shares = std::max(1LL, std::min(8 * sms / pairs, (p.max_moves + round - 1) / round));
   const dim3 rows(static_cast<unsigned>(shares), static_cast<unsigned>(std::min(pairs, 65535LL)),
                   static_cast<unsigned>((pairs + 65534) / 65535));
   return pa::launch_overlapped(pa::evict_rows_kernel, rows, dim3(256), 0, pa::as_stream(stream), p);

@@ -1371,16 +1371,25 @@ __device__ __forceinline__ void weights_rows(const DecodeParams& p, const Weight
     const int h = h_kv * p.G + g;
     float M = kNegInf, L = 0.f;
     bool bad = false;
-    for (int i = lane; i < n_parts; i += 32) {
-      const int c = c_first + i / p.nbs, jj = i % p.nbs;
-      const size_t slot = p.mode == 0 ? static_cast<size_t>(s + c) : static_cast<size_t>(s) * p.max_parts + c;
-      const float* r = p.partials + ((slot * p.nbs + jj) * p.H_q + h) * static_cast<size_t>(D + 4) + D;
-      const float mi = r[0], li = r[1];
-      bad = bad || li < 0.f;
-      if (li > 0.f) {  // (a partial whose sum is NaN is left out, as by the merge)
-        const float mn = fmaxf(M, mi);
-        L = (M == kNegInf ? 0.f : L * ex2(M - mn)) + li * ex2(mi - mn);
-        M = mn;
+    // the partials of one row lie in consecutive (slot, block slot) rows
+    const size_t part0 = p.mode == 0 ? static_cast<size_t>(s + c_first) : static_cast<size_t>(s) * p.max_parts;
+    const float* part = p.partials + (part0 * p.nbs * p.H_q + h) * static_cast<size_t>(D + 4) + D;
+    const size_t part_step = static_cast<size_t>(p.H_q) * (D + 4);
+    for (int i0 = lane; i0 < n_parts; i0 += 128) {  // four of a lane's partials are loaded together
+      float2 ml[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        ml[q] = i0 + 32 * q < n_parts ? *reinterpret_cast<const float2*>(part + (i0 + 32 * q) * part_step)
+                                      : make_float2(kNegInf, 0.f);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float mi = ml[q].x, li = ml[q].y;
+        bad = bad || li < 0.f;
+        if (li > 0.f) {  // (a partial whose sum is NaN is left out, as by the merge)
+          const float mn = fmaxf(M, mi);
+          L = (M == kNegInf ? 0.f : L * ex2(M - mn)) + li * ex2(mi - mn);
+          M = mn;
+        }
       }
     }
     float Mw = M;

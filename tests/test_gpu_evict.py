@@ -92,9 +92,9 @@ def test_head_layouts(H, D):
     _check(workload("bf16", B=2, H_q=H, H_kv=H, D=D, ctx_list=[90, 301]), [90, 301], 64, 1, 16)
 
 
-@pytest.mark.parametrize("n", [4096, 4097, 9000, 20000])
+@pytest.mark.parametrize("n", [4096, 4097, 9000, 20000, 40000, 70000])
 def test_clusters(n):
-    # one, two, four and eight CTAs per (sequence, head)
+    # few and many slots for one CTA, then four and eight CTAs per (sequence, head)
     w = workload("bf16", B=2, H_q=1, H_kv=1, D=64, ctx_list=[n, 37])
     for mode in ("spread", "equal"):
         _check(w, [n, 37], n // 4, 4, n // 16, mode, in_place=mode == "equal")
