@@ -30,8 +30,8 @@
 //     store writes consecutive entries; scores and positions of kept slots are copied (unless in place);
 //  6. movers' scores and positions go to the holes, and the listed rows move, 16 bytes per lane: a lane's
 //     part of a row (which tensor, which 16 bytes) is the same for every row, and a warp has several rows
-//     in flight.  With many slots there are few CTAs and many rows, and a second launch with as many CTAs
-//     as the GPU holds moves them.
+//     in flight.  Where there are few CTAs and many rows, a second launch with as many CTAs as the GPU
+//     holds moves them.
 // Everything is integer comparison and counting in a fixed order: the result does not depend on timing.
 
 #include <algorithm>
@@ -52,6 +52,7 @@ constexpr int kEvMaxContext = 1 << 21;  // so that every word of kept bits has i
 struct EvictParams {
   int B, H, num_blocks, max_blocks, max_ctx, stride, budget, anchors, recent;
   int cluster, cap, max_moves;
+  int rows_apart;  // a second launch moves the rows
   const int32_t* block_tables;
   const int32_t* context_lens;
   const float* scores_in;
@@ -276,9 +277,13 @@ __global__ void __launch_bounds__(T, 1024 / T) evict_kernel(const EvictParams p)
   };
 
   // The lists.  SMALL: where the keys and positions were (at most n / 2 entries each, and nothing reads
-  // keys or positions after the kept words are known).
-  int2* holes = SMALL ? reinterpret_cast<int2*>(dyn) : p.holes + static_cast<size_t>(pair) * p.max_moves;
-  int2* movers = SMALL ? reinterpret_cast<int2*>(own_pos) : p.movers + static_cast<size_t>(pair) * p.max_moves;
+  // keys or positions after the kept words are known), unless a second launch reads them.
+  int2* holes = p.holes + static_cast<size_t>(pair) * p.max_moves;
+  int2* movers = p.movers + static_cast<size_t>(pair) * p.max_moves;
+  if (SMALL && !p.rows_apart) {
+    holes = reinterpret_cast<int2*>(dyn);
+    movers = reinterpret_cast<int2*>(own_pos);
+  }
 
   uint32_t thr = 0;  // keys above it are kept, `need` of those equal to it too
   int need = n, moves = 0;
@@ -541,8 +546,8 @@ __global__ void __launch_bounds__(T, 1024 / T) evict_kernel(const EvictParams p)
     sc_out[to] = sc[from];
     po_out[to] = po ? po[from] : from;
   }
-  if constexpr (SMALL) {
-    move_rows(p, h, holes, movers, moves, warp, W);
+  if (!p.rows_apart) {
+    move_rows(p, h, holes, movers, moves, rank * W + warp, C * W);
   } else if (rank == 0 && tid == 0) {
     p.counts[pair] = moves;
   }
@@ -665,6 +670,14 @@ extern "C" pa_status pa_cache_evict(const pa_cache_desc* desc, void* k_cache, vo
   const bool small = C == 1 && span <= static_cast<size_t>(pa::kEvSmall);
   p.cap = static_cast<int>(small ? span : std::min<size_t>(span, pa::kEvMaxKeys));
   const size_t key_bytes = static_cast<size_t>(p.cap) * (small ? 8 : 4) + span / 8;
+  // A second launch for the rows when this one has too few warps to keep enough of them in flight: for 512
+  // threads a CTA, and for 256 with few pairs or many rows.  Inline and apart: 8 pairs from 4096 slots to
+  // 2048 25 and 17 us, 64 of them 31 and 25, 400 of them 108 and 97; 400 pairs from 2048 to 1024 47 and 53 us,
+  // 64 from 1000 to 900 8.4 and 9.6.
+#ifndef PA_EVICT_APART
+#define PA_EVICT_APART (!small || p.max_moves > (pairs < 3 * sms / 2 ? 256 : 1536))
+#endif
+  p.rows_apart = (PA_EVICT_APART && p.max_moves > 0) ? 1 : 0;
   auto kern = small ? pa::evict_kernel<256, true> : pa::evict_kernel<512, false>;
   if (!pa::ensure_dynamic_smem(reinterpret_cast<const void*>(kern), key_bytes)) return PA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
@@ -682,7 +695,7 @@ extern "C" pa_status pa_cache_evict(const pa_cache_desc* desc, void* k_cache, vo
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return PA_ERR_CUDA;
-  if (small || p.max_moves == 0) return PA_OK;
+  if (!p.rows_apart) return PA_OK;
   // the rows: eight CTAs per SM in all, none with less than a round of its warps' rows
   const long long round = 8LL * 4 * (32 / p.total_units);
   const long long shares = std::max(1LL, std::min(8 * sms / pairs, (p.max_moves + round - 1) / round));

@@ -1304,6 +1304,14 @@ struct WeightsParams {
   int shares;   // CTAs per (sequence, KV head)
 };
 
+// Add a partial (maximum mi, sum li > 0) to a running one; a maximum of NaN or minus infinity adds nothing.
+__device__ __forceinline__ void add_partial(float& M, float& L, float mi, float li) {
+  const float mn = fmaxf(M, mi);
+  if (!(mi > kNegInf)) return;
+  L = (M == kNegInf ? 0.f : L * ex2(M - mn)) + li * ex2(mi - mn);
+  M = mn;
+}
+
 // GP: p.raw_g.  A thread takes positions c0 + tid + 128 i of a chunk; the first chunk's scores are loaded
 // before M and L are known, so that the loads run beside the partials'.
 constexpr int weights_per_thread(int gp) { return gp == 8 ? 4 : 8; }
@@ -1311,7 +1319,7 @@ constexpr int weights_per_thread(int gp) { return gp == 8 ? 4 : 8; }
 template <int D, int GP>
 __device__ __forceinline__ void weights_rows(const DecodeParams& p, const WeightsParams& wp, int grid_x, int y) {
   constexpr int E = D / 32, P = weights_per_thread(GP), CHUNK = 128 * P;
-  __shared__ float sh_m[8], sh_inv[8];
+  __shared__ float sh_m[8], sh_inv[8], sh_x[32][GP];
   __shared__ int sh_bad;
   const int s = blockIdx.x, tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
   const int h_kv = y / wp.shares, share = y - h_kv * wp.shares;
@@ -1366,65 +1374,89 @@ __device__ __forceinline__ void weights_rows(const DecodeParams& p, const Weight
     }
   }
   const int n_parts = (c_last - c_first + 1) * p.nbs;
-  __syncthreads();
-  for (int g = wid; g < p.G; g += 4) {  // one warp per query head: M and L
-    const int h = h_kv * p.G + g;
-    float M = kNegInf, L = 0.f;
-    bool bad = false;
+  // M and L of each query head's row: one warp per head, at most two heads per warp
+  constexpr int HW = (GP + 3) / 4;
+  float M[HW], L[HW];
+  bool bad = false;
+#pragma unroll
+  for (int q = 0; q < HW; ++q) {
+    const int g = wid + 4 * q;
+    M[q] = kNegInf;
+    L[q] = 0.f;
+    if (g >= p.G) continue;
     // the partials of one row lie in consecutive (slot, block slot) rows
     const size_t part0 = p.mode == 0 ? static_cast<size_t>(s + c_first) : static_cast<size_t>(s) * p.max_parts;
-    const float* part = p.partials + (part0 * p.nbs * p.H_q + h) * static_cast<size_t>(D + 4) + D;
+    const float* part = p.partials + (part0 * p.nbs * p.H_q + h_kv * p.G + g) * static_cast<size_t>(D + 4) + D;
     const size_t part_step = static_cast<size_t>(p.H_q) * (D + 4);
     for (int i0 = lane; i0 < n_parts; i0 += 128) {  // four of a lane's partials are loaded together
       float2 ml[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        ml[q] = i0 + 32 * q < n_parts ? *reinterpret_cast<const float2*>(part + (i0 + 32 * q) * part_step)
+      for (int j = 0; j < 4; ++j)
+        ml[j] = i0 + 32 * j < n_parts ? *reinterpret_cast<const float2*>(part + (i0 + 32 * j) * part_step)
                                       : make_float2(kNegInf, 0.f);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float mi = ml[q].x, li = ml[q].y;
-        bad = bad || li < 0.f;
-        if (li > 0.f) {  // (a partial whose sum is NaN is left out, as by the merge)
-          const float mn = fmaxf(M, mi);
-          L = (M == kNegInf ? 0.f : L * ex2(M - mn)) + li * ex2(mi - mn);
-          M = mn;
+      for (int j = 0; j < 4; ++j) {
+        bad = bad || ml[j].y < 0.f;
+        // (a partial whose sum is NaN is left out, as by the merge)
+        if (ml[j].y > 0.f) add_partial(M[q], L[q], ml[j].x, ml[j].y);
+      }
+    }
+  }
+  if (n_sink > lo) {
+    // sinks, 32 at a time: a warp takes every fourth one and all G heads' scores of it, which go to shared
+    // memory (and, where this CTA takes the position up below, beside the other scores)
+    float qv[GP][E];
+#pragma unroll
+    for (int g = 0; g < GP; ++g) {
+      SinkRow<E> x;
+      x.load(p.q + (static_cast<size_t>(s) * p.H_q + h_kv * p.G + min(g, p.G - 1)) * D + lane * E);
+#pragma unroll
+      for (int e = 0; e < E; ++e) qv[g][e] = x.at(e);
+    }
+    for (int t0 = lo; t0 < n_sink; t0 += 32) {
+      const int cnt = min(32, n_sink - t0);
+      __syncthreads();  // the scores of the 32 before have been taken up
+#pragma unroll 2
+      for (int i = wid; i < cnt; i += 4) {
+        SinkRow<E> k;
+        k.load(p.k_sink + ((static_cast<size_t>(s) * p.num_sink + t0 + i) * p.H_kv + h_kv) * D + lane * E);
+        float dot[GP];
+#pragma unroll
+        for (int g = 0; g < GP; ++g) {
+          dot[g] = 0.f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) dot[g] = fmaf(qv[g][e], k.at(e), dot[g]);
+        }
+#pragma unroll
+        for (int mask = 1; mask < 32; mask <<= 1)
+#pragma unroll
+          for (int g = 0; g < GP; ++g) dot[g] += __shfl_xor_sync(0xffffffffu, dot[g], mask);
+        if (lane == 0) {
+#pragma unroll
+          for (int g = 0; g < GP; ++g) {
+            sh_x[i][g] = dot[g] * p.scale_log2;
+            if ((t0 + i) / CHUNK % wp.shares == share) raw[static_cast<size_t>(t0 + i) * GP + g] = dot[g] * p.scale_log2;
+          }
         }
       }
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < HW; ++q)
+        if (wid + 4 * q < p.G && lane < cnt) add_partial(M[q], L[q], sh_x[lane][wid + 4 * q], 1.f);
     }
-    float Mw = M;
+  }
+  bad = __any_sync(0xffffffffu, bad);
+#pragma unroll
+  for (int q = 0; q < HW; ++q) {
+    float Mw = M[q];
 #pragma unroll
     for (int mask = 1; mask < 32; mask <<= 1) Mw = warp_max_xor(Mw, mask);
-    float Lw = L != 0.f ? L * ex2(M - Mw) : 0.f;
+    float Lw = L[q] != 0.f ? L[q] * ex2(M[q] - Mw) : 0.f;
 #pragma unroll
     for (int mask = 1; mask < 32; mask <<= 1) Lw += __shfl_xor_sync(0xffffffffu, Lw, mask);
-    bad = __any_sync(0xffffffffu, bad);
-    if (n_sink > lo) {  // sinks: their scores, stored where this CTA takes them up below
-      const __nv_bfloat16* qrow = p.q + (static_cast<size_t>(s) * p.H_q + h) * D + lane * E;
-      float qv[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) qv[e] = __bfloat162float(qrow[e]);
-      SinkRow<E> k;
-      const __nv_bfloat16* krow = p.k_sink + (static_cast<size_t>(s) * p.num_sink * p.H_kv + h_kv) * D + lane * E;
-      k.load(krow + static_cast<size_t>(lo) * p.H_kv * D);
-      for (int t = lo; t < n_sink; ++t) {
-        const SinkRow<E> kt = k;
-        if (t + 1 < n_sink) k.load(krow + static_cast<size_t>(t + 1) * p.H_kv * D);
-        float dot = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) dot += qv[e] * kt.at(e);
-#pragma unroll
-        for (int mask = 1; mask < 32; mask <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, mask);
-        const float st = dot * p.scale_log2;
-        if (lane == 0 && t / CHUNK % wp.shares == share) raw[static_cast<size_t>(t) * GP + g] = st;
-        const float mn = fmaxf(Mw, st);
-        Lw = (Lw != 0.f ? Lw * ex2(Mw - mn) : 0.f) + ex2(st - mn);
-        Mw = mn;
-      }
-    }
-    if (lane == 0) {
-      sh_m[g] = Mw;
-      sh_inv[g] = Lw > 0.f ? 1.f / Lw : 0.f;  // no sum: the output row is zero, and so are its weights
+    if (lane == 0 && wid + 4 * q < p.G) {
+      sh_m[wid + 4 * q] = Mw;
+      sh_inv[wid + 4 * q] = Lw > 0.f ? 1.f / Lw : 0.f;  // no sum: the output row is zero, and so are its weights
       if (bad) sh_bad = 1;
     }
   }
@@ -1461,7 +1493,7 @@ __device__ __forceinline__ void weights_rows(const DecodeParams& p, const Weight
 template <int D, int WPR, int GP>
 __global__ void __launch_bounds__(128) merge_weights_kernel(const DecodeParams p, const WeightsParams wp, int grid_x) {
   const int y = static_cast<int>(blockIdx.y) - wp.merge_y;
-  if (y < 0) merge_rows<D, WPR, 8>(p, grid_x);
+  if (y < 0) merge_rows<D, WPR, WPR == 4 ? 16 : 8>(p, grid_x);  // (few rows may have hundreds of partials each)
   else weights_rows<D, GP>(p, wp, grid_x, y);
 }
 
@@ -1612,6 +1644,8 @@ pa_status launch(const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, c
   if (launch_overlapped(kern, grid, dim3(pl.threads), pl.smem_bytes, stream, mk, mv, mkp, mvp, p) != PA_OK)
     return PA_ERR_CUDA;
   // few (sequence, head) rows for the SMs (long contexts, small batches): four warps per row
+  if (static_cast<long long>(p.B) * p.H_q < 4LL * std::max(1, sm_count_current()) && p.anchors > 0)
+    return launch_overlapped(merge_kernel<D, 4, 16>, dim3(p.B, p.H_q), dim3(128), 0, stream, p, pl.grid_x);
   if (static_cast<long long>(p.B) * p.H_q < 4LL * std::max(1, sm_count_current()))
     return launch_overlapped(merge_kernel<D, 4, 8>, dim3(p.B, p.H_q), dim3(128), 0, stream, p, pl.grid_x);
   if (p.n_extra > 0)
