@@ -414,12 +414,14 @@ pa_status pa_prefill_step_ws(const pa_cache_desc* desc, void* out, const void* q
  *   scale             finite and > 0 (the tensor-core kernel takes a row's maximum before it scales)
  *   max_context_len   bounds every context_lens[s]; 0 <= max_context_len <= max_blocks_per_seq*16.
  *   workspace         at least pa_prefill_anchored_workspace_size(...) bytes, 256-byte aligned,
- *                     scratch for this call only: caches that are decoded (8-bit, per-token-scaled,
- *                     INT4, with sinks) are decoded into it block by block, once, as by
- *                     pa_prefill_attention_ws, but only the blocks that the chunk can attend, so its
- *                     size goes with W + max_query_len + num_anchor, not with the context.  The size
- *                     is 0 when the call needs none (as pa_prefill_workspace_size; workspace may then
- *                     be NULL) or an argument is invalid.  With anchors and a window, 8-bit caches with
+ *                     scratch for this call only.  With many query rows, caches that are decoded
+ *                     (8-bit, per-token-scaled, INT4, with sinks) are decoded into it block by block,
+ *                     once, as by pa_prefill_attention_ws, but only the blocks that the chunk can
+ *                     attend, so its size goes with W + max_query_len + num_anchor, not with the
+ *                     context.  With few rows the keys of a query tile are split over several CTAs,
+ *                     and it takes their partial rows.  The size is 0 when the call needs none
+ *                     (workspace may then be NULL) or an argument is invalid; ask for it on the
+ *                     device that the call runs on.  With anchors and a window, 8-bit caches with
  *                     per-head scales keep their bare codes there (the scales multiply the scores and
  *                     the output), so that K and V are not rounded; other decoded values are, to bf16.
  * A sequence that breaks pa_prefill_attention's rules, or (with a workspace) has a context beyond

@@ -65,13 +65,23 @@ struct PrefillParams {
   const __nv_bfloat16* k_sink;
   const __nv_bfloat16* v_sink;
   size_t extra_offset;
+  // Split keys (pa_prefill_attention_anchored with few query tiles): `splits` CTAs share a tile's blocks
+  // and leave partial rows part[((s * max_q + token) * H_q + h) * splits + split][D + 4] = (o, m, l), l = -1
+  // after a bad block id, which prefill_join_kernel combines.  1: none.
+  int splits;
+  int max_ctx;  // contexts beyond it are invalid
+  float* part;
 };
+
+__device__ __forceinline__ bool prefill_valid(const PrefillParams& p, int n, int ctx) {
+  return n >= 0 && n <= ctx && n <= p.max_q && ctx <= p.max_blocks * PA_BLOCK_SIZE && ctx <= p.max_ctx;
+}
 
 // The blocks a query tile reads: [0, ab), then [kb0, kb0 + n - ab); ab = 0 without anchors, and
 // when the anchors' blocks reach kb0 (the list is then one run from block 0).  kv_lo: first key of
 // the window part (0 when the anchors reach it); kv_end: one past the last key.
 struct BlockList {
-  int ab, kb0, n, lo;
+  int ab, kb0, n, lo, k0 = 0;
   __device__ __forceinline__ BlockList(const PrefillParams& p, int kv_lo, int kv_end) : lo(kv_lo) {
     kb0 = kv_lo / PA_BLOCK_SIZE;
     ab = p.window > 0 ? (p.anchors + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE : 0;
@@ -81,7 +91,14 @@ struct BlockList {
     }
     n = ab + (kv_end + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE - kb0;
   }
-  __device__ __forceinline__ int block(int k) const { return k < ab ? k : kb0 + k - ab; }
+  __device__ __forceinline__ int block(int k) const { return k + k0 < ab ? k + k0 : kb0 + k + k0 - ab; }
+  // The share `split` of `splits` of the list.
+  __device__ __forceinline__ void cut(int split, int splits) {
+    if (splits == 1) return;
+    const int per = (n + splits - 1) / splits;
+    k0 = min(n, split * per);
+    n = min(per, n - k0);
+  }
   // Whether logical block b holds an attended position outside the sink buffers; the table entry of
   // another block is not looked at (it may have been released).
   __device__ __forceinline__ bool paged(const PrefillParams& p, int b) const {
@@ -252,12 +269,26 @@ struct PrefillRows {
     }
   }
 
-  // reduce l over the quad, divide, write bf16 rows (zeros after a bad block id)
-  __device__ __forceinline__ void finish(const PrefillParams& p, int qs, int h_kv) {
+  // reduce l over the quad, divide, write bf16 rows (zeros after a bad block id), or partial rows
+  __device__ __forceinline__ void finish(const PrefillParams& p, int s, int qs, int h_kv, int split) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
       l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
+    }
+    if (p.splits > 1) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (!row_ok[half]) continue;
+        const int r = t4 + 8 * half;
+        float* row = p.part + ((static_cast<size_t>(s) * p.max_q + wt0 + r / p.G) * p.H_q + h_kv * p.G + r % p.G) *
+                                  p.splits * (D + 4) + static_cast<size_t>(split) * (D + 4);
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+          *reinterpret_cast<float2*>(row + i * 8 + 2 * tq) = make_float2(o[i][2 * half], o[i][2 * half + 1]);
+        if (tq == 0) *reinterpret_cast<float2*>(row + D) = make_float2(m[half], bad ? -1.f : l[half]);
+      }
+      return;
     }
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -284,15 +315,14 @@ __global__ void __launch_bounds__(kPfThreads)
   __shared__ int bad_stage[kPfStages];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int s = blockIdx.y, h_kv = blockIdx.z, tile = blockIdx.x;
+  const int s = blockIdx.y, h_kv = blockIdx.z / p.splits, split = blockIdx.z % p.splits, tile = blockIdx.x;
   // launched with programmatic dependent launch: the previous kernel of the stream may still be
   // writing any input (q, lengths, tables, cache), so everything below waits for it
   grid_dep_wait();
   const int qs = p.q_start[s];
   const int n = p.q_start[s + 1] - qs;
   const int ctx = p.context_lens[s];
-  const bool valid = n >= 0 && n <= ctx && n <= p.max_q && ctx <= p.max_blocks * PA_BLOCK_SIZE;
-  if (!valid) {
+  if (!prefill_valid(p, n, ctx)) {
     if (tile == 0 && h_kv == 0 && tid == 0) set_error(p.err, PA_EFLAG_CTX_OVERFLOW);
     // zero the rows this CTA would have produced (those inside the query range it can see)
     const int rows = min(max(n, 0), p.max_q);
@@ -306,7 +336,8 @@ __global__ void __launch_bounds__(kPfThreads)
   const int first_pos = ctx - n;
   const int t_end = min(n, t0 + p.q_tile);
   const int kv_end = first_pos + t_end;  // keys [kv_lo, kv_end) are visible to this tile
-  const BlockList bl(p, key_lo(p, first_pos + t0), kv_end);  // the logical blocks read
+  BlockList bl(p, key_lo(p, first_pos + t0), kv_end);  // the logical blocks read
+  bl.cut(split, p.splits);
   const int n_blocks = bl.n;
 
   if (tid == 0) {
@@ -378,7 +409,7 @@ __global__ void __launch_bounds__(kPfThreads)
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[st]);
   }
-  w.finish(p, qs, h_kv);
+  w.finish(p, s, qs, h_kv, split);
 }
 
 // ------------------------------------------------------------------------------------
@@ -506,13 +537,12 @@ __global__ void __launch_bounds__(kPfWarps * 32)
   __shared__ int bad_blk[2];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int s = blockIdx.y, h_kv = blockIdx.z, tile = blockIdx.x;
+  const int s = blockIdx.y, h_kv = blockIdx.z / p.splits, split = blockIdx.z % p.splits, tile = blockIdx.x;
   grid_dep_wait();  // the previous kernel of the stream may still be writing any input
   const int qs = p.q_start[s];
   const int n = p.q_start[s + 1] - qs;
   const int ctx = p.context_lens[s];
-  const bool valid = n >= 0 && n <= ctx && n <= p.max_q && ctx <= p.max_blocks * PA_BLOCK_SIZE;
-  if (!valid) {
+  if (!prefill_valid(p, n, ctx)) {
     if (tile == 0 && h_kv == 0 && tid == 0) set_error(p.err, PA_EFLAG_CTX_OVERFLOW);
     const int rows = min(max(n, 0), p.max_q);
     for (int t = tile * p.q_tile + warp; t < min(rows, (tile + 1) * p.q_tile); t += kPfWarps)
@@ -525,7 +555,8 @@ __global__ void __launch_bounds__(kPfWarps * 32)
   const int first_pos = ctx - n;
   const int t_end = min(n, t0 + p.q_tile);
   const int kv_end = first_pos + t_end;
-  const BlockList bl(p, key_lo(p, first_pos + t0), kv_end);
+  BlockList bl(p, key_lo(p, first_pos + t0), kv_end);
+  bl.cut(split, p.splits);
   const int n_blocks = bl.n;
   const int32_t* trow = p.block_tables + static_cast<size_t>(s) * p.max_blocks;
 
@@ -567,7 +598,53 @@ __global__ void __launch_bounds__(kPfWarps * 32)
     if (bad_blk[k & 1]) w.bad = true;
     else w.block(p, wk, wk + TILE, bl.block(k) * PA_BLOCK_SIZE, kv_end);
   }
-  w.finish(p, qs, h_kv);
+  w.finish(p, s, qs, h_kv, split);
+}
+
+// Joins the partial rows of split keys, one warp per (query token, head): out = sum 2^(m_i - M) o_i /
+// sum 2^(m_i - M) l_i (zeros after a bad block id or without a key).  At most 32 splits, a lane each.
+template <int D>
+__global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillParams p) {
+  constexpr int E = D / 32;
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31;
+  const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int h = static_cast<int>(row % p.H_q), tok = static_cast<int>(row / p.H_q % p.max_q);
+  const long long s = row / p.H_q / p.max_q;
+  if (s >= p.B) return;
+  const int qs = p.q_start[s], n = p.q_start[s + 1] - qs;
+  if (!prefill_valid(p, n, p.context_lens[s]) || tok >= n) return;
+  const float* part = p.part + static_cast<size_t>(row) * p.splits * (D + 4);
+  float2 ml = make_float2(kNegInfP, 0.f);
+  if (lane < p.splits) ml = *reinterpret_cast<const float2*>(part + static_cast<size_t>(lane) * (D + 4) + D);
+  const bool bad = __any_sync(0xffffffffu, ml.y < 0.f);
+  float M = ml.y > 0.f ? ml.x : kNegInfP;
+#pragma unroll
+  for (int mask = 1; mask < 32; mask <<= 1) M = warp_max_xor(M, mask);
+  const float w = ml.y > 0.f ? ex2(ml.x - M) : 0.f;
+  float L = w * ml.y;
+#pragma unroll
+  for (int mask = 1; mask < 32; mask <<= 1) L += __shfl_xor_sync(0xffffffffu, L, mask);
+  float acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < p.splits; ++i) {
+    const float wi = __shfl_sync(0xffffffffu, w, i);
+    float v[E];
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float2 x = *reinterpret_cast<const float2*>(part + static_cast<size_t>(i) * (D + 4) + lane * E + e);
+      v[e] = x.x, v[e + 1] = x.y;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] += wi != 0.f ? wi * v[e] : 0.f;
+  }
+  const float inv = (bad || !(L > 0.f)) ? 0.f : 1.f / L;
+  __nv_bfloat16* orow = p.out + (static_cast<size_t>(qs + tok) * p.H_q + h) * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t*>(orow + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
 }
 
 // ------------------------------------------------------------------------------------
@@ -703,8 +780,44 @@ PrefillParams prefill_params(const pa_cache_desc* desc, void* out, const void* q
   p.v_scales = desc->v_scales;
   p.k_sink = static_cast<const __nv_bfloat16*>(desc->k_sink);
   p.v_sink = static_cast<const __nv_bfloat16*>(desc->v_sink);
+  p.splits = 1;
+  p.max_ctx = 0x7FFFFFFF;
+  p.part = nullptr;
   p.extra_offset = is_int4(desc) ? int4_params_offset(desc) : (has_token_scales(desc) ? token_scales_offset(desc) : 0);
   return p;
+}
+
+// The warp-MMA kernels (bf16 caches without sinks by TMA, every other one decoded block by block), with
+// the keys of a tile split over p.splits CTAs.
+pa_status prefill_warps(const pa_cache_desc* desc, const PrefillParams& p, const void* k_cache, const void* v_cache,
+                        void* stream) {
+  const int D = desc->head_dim, nc = D * 2 / 128;
+  const bool dq = is_quantized(desc) || desc->num_sink > 0;  // decoded per block (prefill_dq_kernel)
+  const long long slots = static_cast<long long>(desc->num_blocks) * PA_BLOCK_SIZE;
+  CUtensorMap mk, mv;
+  if (!dq && (!encode_cache_map(&mk, k_cache, 2, desc->num_kv_heads * nc, 1, slots) ||
+              !encode_cache_map(&mv, v_cache, 2, desc->num_kv_heads * nc, 1, slots)))
+    return PA_ERR_CUDA;
+  const dim3 grid((p.max_q + p.q_tile - 1) / p.q_tile, p.B, p.H_kv * p.splits);
+  cudaStream_t s = as_stream(stream);
+  pa_status st;
+  if (dq) {  // 8-bit and INT4 caches have head_dim 128 (validate_desc)
+    const dim3 block(kPfWarps * 32);
+    if (is_int4(desc)) st = launch_overlapped(prefill_dq_kernel<128, 2>, grid, block, 0, s, p);
+    else if (has_token_scales(desc)) st = launch_overlapped(prefill_dq_kernel<128, 3>, grid, block, 0, s, p);
+    else if (is_quantized(desc)) st = launch_overlapped(prefill_dq_kernel<128, 1>, grid, block, 0, s, p);
+    else if (D == 128) st = launch_overlapped(prefill_dq_kernel<128, 0>, grid, block, 0, s, p);
+    else st = launch_overlapped(prefill_dq_kernel<64, 0>, grid, block, 0, s, p);
+  } else if (D == 128) {
+    st = launch_overlapped(prefill_kernel<128>, grid, dim3(kPfThreads), 0, s, mk, mv, p);
+  } else {
+    st = launch_overlapped(prefill_kernel<64>, grid, dim3(kPfThreads), 0, s, mk, mv, p);
+  }
+  if (st != PA_OK || p.splits == 1) return st;
+  const long long rows = static_cast<long long>(p.B) * p.max_q * p.H_q;
+  const dim3 join(static_cast<unsigned>((rows + 7) / 8));
+  return D == 128 ? launch_overlapped(prefill_join_kernel<128>, join, dim3(256), 0, s, p)
+                  : launch_overlapped(prefill_join_kernel<64>, join, dim3(256), 0, s, p);
 }
 
 // pa_prefill_attention after its checks; step: the previous kernel is this step's append.
@@ -712,36 +825,16 @@ pa_status prefill_launch(const pa_cache_desc* desc, void* out, const void* q, co
                          const void* v_cache, const int32_t* block_tables, const int32_t* q_start,
                          const int32_t* context_lens, int max_query_len, float scale, int32_t* err_flag,
                          void* stream, bool step, int anchors = 0) {
-  const int D = desc->head_dim;
   const int G = desc->num_q_heads / desc->num_kv_heads;
-  const bool dq = is_quantized(desc) || desc->num_sink > 0;  // decoded per block (prefill_dq_kernel)
+  const bool dq = is_quantized(desc) || desc->num_sink > 0;
 #ifndef PA_PREFILL_WARP_MMA_ONLY
-  if (!dq && D == 128 && (G & (G - 1)) == 0)  // the tensor-core (tcgen05) kernel
+  if (!dq && desc->head_dim == 128 && (G & (G - 1)) == 0)  // the tensor-core (tcgen05) kernel
     return launch_prefill_tc(desc, out, q, k_cache, v_cache, block_tables, q_start, context_lens, max_query_len,
                              scale, err_flag, as_stream(stream), step, anchors);
 #endif
   (void)step;  // the warp-MMA kernel waits for its predecessor before it starts
-  const int nc = D * 2 / 128;
-  const long long slots = static_cast<long long>(desc->num_blocks) * PA_BLOCK_SIZE;
-  CUtensorMap mk, mv;
-  if (!dq && (!encode_cache_map(&mk, k_cache, 2, desc->num_kv_heads * nc, 1, slots) ||
-              !encode_cache_map(&mv, v_cache, 2, desc->num_kv_heads * nc, 1, slots)))
-    return PA_ERR_CUDA;
-  const PrefillParams p = prefill_params(desc, out, q, k_cache, v_cache, block_tables, q_start, context_lens,
-                                         max_query_len, scale, err_flag, anchors);
-  const dim3 grid((max_query_len + p.q_tile - 1) / p.q_tile, p.B, p.H_kv);
-  cudaStream_t s = as_stream(stream);
-  if (dq) {  // 8-bit and INT4 caches have head_dim 128 (validate_desc)
-    const dim3 block(kPfWarps * 32);
-    if (is_int4(desc)) return launch_overlapped(prefill_dq_kernel<128, 2>, grid, block, 0, s, p);
-    if (has_token_scales(desc)) return launch_overlapped(prefill_dq_kernel<128, 3>, grid, block, 0, s, p);
-    if (is_quantized(desc)) return launch_overlapped(prefill_dq_kernel<128, 1>, grid, block, 0, s, p);
-    if (D == 128) return launch_overlapped(prefill_dq_kernel<128, 0>, grid, block, 0, s, p);
-    return launch_overlapped(prefill_dq_kernel<64, 0>, grid, block, 0, s, p);
-  }
-  if (D == 128)
-    return launch_overlapped(prefill_kernel<128>, grid, dim3(kPfThreads), 0, s, mk, mv, p);
-  return launch_overlapped(prefill_kernel<64>, grid, dim3(kPfThreads), 0, s, mk, mv, p);
+  return prefill_warps(desc, prefill_params(desc, out, q, k_cache, v_cache, block_tables, q_start, context_lens,
+                                            max_query_len, scale, err_flag, anchors), k_cache, v_cache, stream);
 }
 
 // Bytes of pa_prefill_attention_ws's workspace (and the bf16 pool's blocks per sequence in *mb):
@@ -767,20 +860,87 @@ size_t prefill_ws_bytes(const pa_cache_desc* d, int max_ctx, int* mb_out) {
 #endif
 }
 
-// The same for pa_prefill_attention_anchored, whose pool holds *cap blocks per sequence: the anchors'
-// blocks and those of the positions that a chunk of max_q queries can attend through its window.
-size_t prefill_anchored_ws_bytes(const pa_cache_desc* d, int max_q, int max_ctx, int anchors, int* mb_out,
-                                 int* cap_out) {
-  int mb = 0;
-  if (max_q < 0 || anchors < 0 || prefill_ws_bytes(d, max_ctx, &mb) == 0) return 0;
-  long long cap = mb;
+// How pa_prefill_attention_anchored runs: the tensor-core kernel, over a decoded copy of *cap blocks per
+// sequence (the anchors' blocks and those of the positions that a chunk of max_q queries can attend through
+// its window) where the cache needs one; or the warp-MMA kernels with a tile's keys split.
+struct AnchoredPlan {
+  bool warps, expand;
+  int mb, cap, splits;
+  size_t bytes;  // workspace
+};
+
+// The choice goes by the time that either takes, in microseconds, fitted to 108 shapes (1 to 16 sequences,
+// chunks of 1 to 512 tokens, windows of 64 to 4096, 1, 4 and 8 query heads per KV head; mean error 10 %):
+//   warp-MMA  6, and 3 for the join; per block of a CTA's share 0.04 by TMA, 0.45 decoded; per block of all
+//             CTAs over the SMs 0.45 and 0.54.  A CTA has 4 x 16 / G query tokens;
+//   tcgen05   9, and 2 per tile of 8 blocks of an SM's items of 256 query rows; the decoded copy 5 and its
+//             bytes at 4.8 TB/s.
+// One sequence's chunk of 8 tokens over a window of 4096, 32/8 heads: 18 against 71; 16 sequences' chunks of
+// 32: 233 against 70.
+bool anchored_plan(const pa_cache_desc* d, int max_q, int max_ctx, int anchors, AnchoredPlan* pl) {
+  if (validate_desc(d) != PA_OK || max_q < 0 || anchors < 0 || max_ctx < 0 ||
+      static_cast<long long>(max_ctx) > static_cast<long long>(d->max_blocks_per_seq) * PA_BLOCK_SIZE)
+    return false;
+  *pl = AnchoredPlan{};
+  pl->splits = 1;
+  const int G = d->num_q_heads / d->num_kv_heads;
+  const bool dq = is_quantized(d) || d->num_sink > 0;
+  bool tc = d->head_dim == 128 && (G & (G - 1)) == 0;
+#ifdef PA_PREFILL_WARP_MMA_ONLY
+  tc = false;
+#endif
+  const size_t copy = prefill_ws_bytes(d, max_ctx, &pl->mb);  // 0: no copy wanted or possible
+  if (tc && dq && copy == 0) tc = false;
+  pl->expand = tc && dq;
+  long long cap = pl->mb;
+  const long long mb = std::max<long long>(1, (static_cast<long long>(max_ctx) + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE);
+  long long span = mb;  // blocks that a chunk can attend
   if (d->sliding_window > 0)
-    cap = std::min(cap, (static_cast<long long>(std::min(anchors, max_ctx)) + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE +
-                            (static_cast<long long>(d->sliding_window) + max_q) / PA_BLOCK_SIZE + 2);
-  *mb_out = mb;
-  *cap_out = static_cast<int>(cap);
-  const size_t table = (static_cast<size_t>(d->num_seqs) * mb * 4 + 255) / 256 * 256;
-  return table + 2 * (static_cast<size_t>(d->num_seqs) * cap * PA_BLOCK_SIZE * d->num_kv_heads * 128 * 2);
+    span = std::min(span, (static_cast<long long>(std::min(anchors, max_ctx)) + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE +
+                              (static_cast<long long>(d->sliding_window) + max_q) / PA_BLOCK_SIZE + 2);
+  cap = std::min(cap, span);
+  pl->cap = static_cast<int>(cap);
+  const int sms = sm_count_current() > 0 ? sm_count_current() : 152;
+  // (without anchors the call is pa_prefill_attention_ws and runs as that does)
+  if (anchors > 0 && d->sliding_window > 0 && max_q > 0 && d->num_seqs > 0) {
+    const int q_tile = kPfWarps * (16 / G), item = 256 / G;  // query tokens of a warp-MMA CTA, of a tcgen05 item
+    const double pairs = static_cast<double>(d->num_seqs) * d->num_kv_heads;
+    // blocks that one tile of `tokens` queries reads
+    auto reach = [&](int tokens) {
+      return static_cast<double>(std::min(span, (static_cast<long long>(std::min(anchors, max_ctx)) + PA_BLOCK_SIZE - 1) /
+                                                        PA_BLOCK_SIZE +
+                                                    (static_cast<long long>(d->sliding_window) + std::min(max_q, tokens)) /
+                                                        PA_BLOCK_SIZE + 2));
+    };
+    const double ctas = pairs * ((max_q + q_tile - 1) / q_tile), blocks = reach(q_tile);
+    // shares of at least 8 blocks, no more CTAs than the GPU holds at once (by their registers)
+    const double held = (dq || d->head_dim == 64 ? 3.0 : 2.0) * sms;
+    const int splits = static_cast<int>(std::max(1.0, std::min({32.0, std::ceil(blocks / 8), held / ctas})));
+    const double warps_us = 6 + (splits > 1 ? 3 : 0) + (dq ? 0.45 : 0.04) * std::ceil(blocks / splits) +
+                            (dq ? 0.54 : 0.45) * ctas * blocks / sms;
+    const double copy_bytes = static_cast<double>(d->num_seqs) * span * PA_BLOCK_SIZE * d->num_kv_heads * 768;
+    const double rounds = std::ceil(pairs * ((max_q + item - 1) / item) / sms);
+    const double tc_us = 9 + 2 * rounds * std::ceil(reach(item) / 8) + (dq ? 5 + copy_bytes / 4.8e6 : 0);
+#ifdef PA_PREFILL_ANCHORED_WARPS
+    pl->warps = PA_PREFILL_ANCHORED_WARPS || !tc;
+#else
+    pl->warps = !tc || warps_us < tc_us;
+#endif
+    if (pl->warps) {
+      pl->splits = splits;
+      if (static_cast<long long>(d->num_kv_heads) * splits > 65535) pl->splits = 1;
+    }
+  }
+  if (pl->warps) {
+    pl->expand = false;
+    pl->bytes = pl->splits == 1 ? 0
+                                : static_cast<size_t>(d->num_seqs) * max_q * d->num_q_heads * pl->splits *
+                                      (d->head_dim + 4) * sizeof(float);
+  } else if (pl->expand) {
+    const size_t table = (static_cast<size_t>(d->num_seqs) * pl->mb * 4 + 255) / 256 * 256;
+    pl->bytes = table + 2 * (static_cast<size_t>(d->num_seqs) * cap * PA_BLOCK_SIZE * d->num_kv_heads * 128 * 2);
+  }
+  return true;
 }
 
 // The expanded path: decode every attended block once into the workspace's bf16 pool, then the
@@ -856,8 +1016,8 @@ extern "C" pa_status pa_prefill_attention_ws(const pa_cache_desc* desc, void* ou
 
 extern "C" size_t pa_prefill_anchored_workspace_size(const pa_cache_desc* desc, int max_query_len,
                                                      int max_context_len, int num_anchor) {
-  int mb = 0, cap = 0;
-  return pa::prefill_anchored_ws_bytes(desc, max_query_len, max_context_len, num_anchor, &mb, &cap);
+  pa::AnchoredPlan pl;
+  return pa::anchored_plan(desc, max_query_len, max_context_len, num_anchor, &pl) ? pl.bytes : 0;
 }
 
 extern "C" pa_status pa_prefill_attention_anchored(const pa_cache_desc* desc, void* out, const void* q,
@@ -874,21 +1034,31 @@ extern "C" pa_status pa_prefill_attention_anchored(const pa_cache_desc* desc, vo
   if (num_anchor < 0 || !(scale > 0.f) || max_context_len < 0 ||
       static_cast<long long>(max_context_len) > static_cast<long long>(desc->max_blocks_per_seq) * PA_BLOCK_SIZE)
     return PA_ERR_INVALID_ARG;
-  int mb = 0, cap = 0;
-  const size_t need = pa::prefill_anchored_ws_bytes(desc, max_query_len, max_context_len, num_anchor, &mb, &cap);
-  if (need > 0) {
+  pa::AnchoredPlan pl;
+  if (!pa::anchored_plan(desc, max_query_len, max_context_len, num_anchor, &pl)) return PA_ERR_INVALID_ARG;
+  if (pl.bytes > 0) {
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return PA_ERR_INVALID_ARG;
-    if (workspace_bytes < need) return PA_ERR_WORKSPACE_TOO_SMALL;
+    if (workspace_bytes < pl.bytes) return PA_ERR_WORKSPACE_TOO_SMALL;
   }
   if (!work) return PA_OK;
   // no position lies past the table, and anchors + 15 must stay within an int
   const int anchors = static_cast<int>(std::min<long long>(
       num_anchor, std::min(static_cast<long long>(desc->max_blocks_per_seq) * PA_BLOCK_SIZE, 0x7FFFFF00LL)));
-  if (need == 0)
+  if (pl.warps) {
+    pa::PrefillParams p = pa::prefill_params(desc, out, q, k_cache, v_cache, block_tables, q_start, context_lens,
+                                             max_query_len, scale, err_flag, anchors);
+    p.splits = pl.splits;
+    if (pl.splits > 1) {
+      p.max_ctx = max_context_len;
+      p.part = static_cast<float*>(workspace);
+    }
+    return pa::prefill_warps(desc, p, k_cache, v_cache, stream);
+  }
+  if (!pl.expand)
     return pa::prefill_launch(desc, out, q, k_cache, v_cache, block_tables, q_start, context_lens, max_query_len,
                               scale, err_flag, stream, false, anchors);
   return pa::prefill_expanded(desc, out, q, k_cache, v_cache, block_tables, q_start, context_lens, max_query_len,
-                              scale, mb, workspace, err_flag, stream, cap, anchors);
+                              scale, pl.mb, workspace, err_flag, stream, pl.cap, anchors);
 }
 
 extern "C" pa_status pa_prefill_step_ws(const pa_cache_desc* desc, void* out, const void* q, void* k_cache,

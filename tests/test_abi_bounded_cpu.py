@@ -76,22 +76,29 @@ def test_anchored_decode():
 
 @host_only
 def test_anchored_prefill():
-    assert N.pa_prefill_anchored_workspace_size(_desc(), 64, 1600, 4) == 0       # bf16 without sinks
-    assert N.pa_prefill_anchored_workspace_size(_desc(head_dim=64), 64, 1600, 4) == 0
+    # many rows, the tensor-core kernel: bf16 caches without sinks need no workspace
+    assert N.pa_prefill_anchored_workspace_size(_desc(), 256, 1600, 4) == 0
     d = _desc(**QUANT)
-    # a dense table of 100 entries a sequence and, per sequence, the blocks that 64 queries of a
-    # 256-token window and 20 anchors can attend: 2 + (256 + 64) / 16 + 2
-    def size(blocks, mb):
+    # a dense table of 100 entries a sequence and, per sequence, the blocks that 256 queries of a
+    # 256-token window and 20 anchors can attend: 2 + (256 + 256) / 16 + 2
+    def copy(blocks, mb):
         return (8 * mb * 4 + 255) // 256 * 256 + 2 * 8 * blocks * 16 * 8 * 128 * 2
-    assert N.pa_prefill_anchored_workspace_size(d, 64, 1600, 20) == size(24, 100)
-    assert N.pa_prefill_anchored_workspace_size(d, 64, 300, 20) == size(19, 19)  # never more than the context
+    assert N.pa_prefill_anchored_workspace_size(d, 256, 1600, 20) == copy(36, 100)
+    assert N.pa_prefill_anchored_workspace_size(d, 256, 400, 20) == copy(25, 25)  # never more than the context
+    # few rows: a tile's keys split; per query row and share of the keys head_dim + 4 floats.  One query of
+    # 8 x 8 KV heads is 64 CTAs over 2 + (256 + 1) / 16 + 2 = 20 blocks: three shares of at least 8 blocks
+    assert N.pa_prefill_anchored_workspace_size(_desc(), 1, 1600, 20) == 8 * 1 * 32 * 3 * 132 * 4
+    assert N.pa_prefill_anchored_workspace_size(_desc(head_dim=64), 1, 1600, 20) == 8 * 1 * 32 * 3 * 68 * 4
+    assert N.pa_prefill_anchored_workspace_size(_desc(num_q_heads=24), 1, 1600, 20) == 8 * 1 * 24 * 3 * 132 * 4
+    # without anchors or a window the call is pa_prefill_attention_ws
     whole = _desc(sliding_window=0, **QUANT)
     assert N.pa_prefill_anchored_workspace_size(whole, 64, 1600, 20) == N.pa_prefill_workspace_size(whole, 1600)
+    assert N.pa_prefill_anchored_workspace_size(_desc(), 1, 1600, 0) == 0
     for bad in ((-1, 1600, 4), (64, -1, 4), (64, 1601, 4), (64, 1600, -1)):
         assert N.pa_prefill_anchored_workspace_size(d, *bad) == 0
-    need = size(24, 100)
+    need = copy(36, 100)
 
-    def call(out=FAKE, q_start=FAKE, max_q=64, max_ctx=1600, scale=0.1, anchors=20, ws=FAKE, n=need, desc=d):
+    def call(out=FAKE, q_start=FAKE, max_q=256, max_ctx=1600, scale=0.1, anchors=20, ws=FAKE, n=need, desc=d):
         N.pa_prefill_attention_anchored(desc, out, FAKE, FAKE, FAKE, FAKE, q_start, FAKE, max_q, max_ctx, scale, anchors,
                                         ws, n, None, 0)
 
@@ -101,7 +108,9 @@ def test_anchored_prefill():
         (dict(max_ctx=1601), N.PA_ERR_INVALID_ARG), (dict(scale=0.0), N.PA_ERR_INVALID_ARG),
         (dict(scale=-0.1), N.PA_ERR_INVALID_ARG), (dict(scale=float("nan")), N.PA_ERR_INVALID_ARG),
         (dict(ws=0), N.PA_ERR_INVALID_ARG), (dict(ws=FAKE + 16), N.PA_ERR_INVALID_ARG),
-        (dict(n=need - 1), N.PA_ERR_WORKSPACE_TOO_SMALL)])
+        (dict(n=need - 1), N.PA_ERR_WORKSPACE_TOO_SMALL),
+        (dict(max_q=1, desc=_desc(), n=1000), N.PA_ERR_WORKSPACE_TOO_SMALL),
+        (dict(max_q=1, desc=_desc(), ws=0), N.PA_ERR_INVALID_ARG)])
     odd = _desc(num_sink=4, k_sink=FAKE + 8, v_sink=FAKE, **QUANT)
     _refused(call, dict(desc=odd, n=1 << 40), [(dict(), N.PA_ERR_INVALID_ARG)])  # sink rows are read 16 bytes at a time
     call(desc=_desc(num_seqs=0, **QUANT))

@@ -298,6 +298,122 @@ def test_prefill_bad_tables_and_lengths_zero_their_rows_only(kind):
     assert np.array_equal(out[:5], good[:5]) and np.array_equal(out[15:20], good[15:20])
 
 
+# Chunks with many rows run on the tensor-core kernel (over a decoded copy for caches that need one); the
+# cases above have few rows and run on the warp-level kernels with their keys split.
+WIDE_CTX, WIDE_CHUNK = [256, 300, 333, 258, 410, 277, 500, 301], np.array([256, 200, 256, 1, 255, 130, 256, 256])
+
+
+def _wide(kind, sinks=0, **kw):
+    return workload(kind, sinks=sinks, B=8, H_q=32, H_kv=8, ctx_list=WIDE_CTX, **kw)
+
+
+def _copy_bytes(g, max_q, max_ctx, anchors, window):
+    # the decoded copy: a dense table and, per sequence, the blocks that the chunk can attend
+    mb = -(-max_ctx // 16)
+    cap = min(mb, -(-min(anchors, max_ctx) // 16) + (window + max_q) // 16 + 2)
+    return -(-g.w.B * mb * 4 // 256) * 256 + 2 * g.w.B * cap * 16 * g.w.H_kv * 128 * 2
+
+
+@pytest.mark.parametrize("window,anchors", [(1, 1), (16, 4), (50, 16), (50, 17), (37, 100), (130, 130), (300, 3)])
+def test_prefill_many_rows(window, anchors):
+    _prefill_case(_wide("bf16"), WIDE_CHUNK, window, anchors)
+
+
+@pytest.mark.parametrize("kind,sinks,anchors", [("bf16", 4, 4), ("bf16", 20, 40), ("fp8", 0, 4), ("fp8", 4, 4),
+                                                ("fp8", 4, 21), ("fp8tok", 4, 4), ("int4", 0, 20)])
+def test_prefill_many_rows_of_decoded_caches(kind, sinks, anchors):
+    w = _wide(kind, sinks)
+    g, _, _, _ = _prefill_case(w, WIDE_CHUNK, 45, anchors)
+    assert N.pa_prefill_anchored_workspace_size(g.desc, 256, 500, anchors) == _copy_bytes(g, 256, 500, anchors, 45)
+
+
+def test_prefill_many_rows_scales_of_either_sign():
+    w = _wide("fp8", 5)
+    w.k_scales[1] *= -1
+    w.v_scales[2] *= -1
+    _prefill_case(w, WIDE_CHUNK, 45, 7)
+
+
+def test_prefill_many_rows_eight_heads_per_kv_head_and_one():
+    for H_q, H_kv, chunk in ((64, 8, 100), (16, 16, 256)):
+        w = workload("bf16", B=8, H_q=H_q, H_kv=H_kv, ctx_list=WIDE_CTX)
+        _prefill_case(w, np.minimum(WIDE_CHUNK, chunk), 60, 20)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_prefill_many_rows_bad_tables_and_lengths(kind):
+    w = _wide(kind)
+    g, _, q, q_start = _prefill_case(w, WIDE_CHUNK, 20, 4)
+    good = prefill(g, q.cuda(), q_start, w.ctx_old, 256, 4)
+    g.tables[1, 0] = w.num_blocks           # the anchors' block
+    g.tables[2, (333 - 1) // 16] = -1       # the last block
+    g.tables_dev.copy_(torch.from_numpy(g.tables))
+    ctx = w.ctx_old.copy()
+    ctx[4] = 254  # 255 queries of a sequence of 254
+    out = prefill(g, q.cuda(), q_start, ctx, 256, 4, max_ctx=500)
+    assert g.err_bits() == N.PA_EFLAG_BAD_BLOCK_ID | N.PA_EFLAG_CTX_OVERFLOW
+    last = q_start[3] - 16  # sequence 2: every query tile whose keys include its last block
+    assert np.all(out[q_start[1]:q_start[2]][100:] == 0) and np.all(out[last:q_start[3]] == 0)
+    assert np.all(out[q_start[4]:q_start[5]] == 0)
+    for s in (0, 3, 5, 6, 7):
+        assert np.array_equal(out[q_start[s]:q_start[s + 1]], good[q_start[s]:q_start[s + 1]])
+
+
+def test_prefill_few_rows_over_a_long_window():
+    # up to 32 shares of the keys, one of them empty, and sequences without keys in some
+    for chunk, G in (([1, 3], 1), ([8, 2], 4), ([5, 7], 7)):
+        w = workload("bf16", B=2, H_q=2 * G, H_kv=2, D=128 if G < 7 else 64, ctx_list=[3500, 40])
+        _prefill_case(w, np.array(chunk), 3000, 130)
+    w = workload("fp8", B=1, sinks=4, H_q=12, H_kv=4, ctx_list=[1900])
+    _prefill_case(w, np.array([5]), 1500, 40)
+
+
+def test_prefill_replayed_from_a_graph_on_another_stream():
+    w = workload("bf16", B=3, ctx_list=[200, 333, 500])
+    g, o = states(w, 100)
+    q_start = np.array([0, 3, 4, 9])
+    q = torch.randn(9, w.H_q, w.D, generator=torch.Generator().manual_seed(9)).to(torch.bfloat16)
+    out = torch.zeros(9, w.H_q, w.D, dtype=torch.bfloat16, device="cuda")
+    n = N.pa_prefill_anchored_workspace_size(g.desc, 5, 500, 20)
+    assert n > 0  # keys split
+    ws, ctx, qd, qs = torch.empty(n, dtype=torch.uint8, device="cuda"), gpu(w.ctx_old), q.cuda(), gpu(q_start)
+
+    def call():
+        N.pa_prefill_attention_anchored(g.desc, out, qd, g.k, g.v, g.tables_dev, qs, ctx, 5, 500, w.scale, 20, ws, n, g.err)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            call()
+    torch.cuda.synchronize()
+    qv = O.bf16_bits_to_f64(bf16_bits(q))
+    for lens in ([200, 333, 500], [3, 60, 499]):
+        ctx.copy_(gpu(lens))
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        for s, c in enumerate(lens):
+            rows = slice(q_start[s], q_start[s + 1])
+            mask = O.anchored_mask(c, q_start[s + 1] - q_start[s], 100, 20)
+            K, V = O.gather_positions(o.cache, s, o.tables[s], np.arange(c))
+            ref, mag = O.masked_attention(qv[rows], K, V, w.scale, mask)
+            assert_within(to_f64(out)[rows], ref, tolerance(ref, mag), f"replay at {lens}, sequence {s}")
+    assert g.err_bits() == 0
+
+
+def test_prefill_context_beyond_the_declared_one():
+    w = workload("bf16", B=2, ctx_list=[400, 300])
+    g, _ = states(w, 200)
+    q = torch.randn(4, w.H_q, w.D, generator=torch.Generator().manual_seed(9)).to(torch.bfloat16).cuda()
+    out = prefill(g, q, np.array([0, 2, 4]), w.ctx_old, 2, 20, max_ctx=399)
+    assert N.pa_prefill_anchored_workspace_size(g.desc, 2, 399, 20) > 0
+    assert g.err_bits() == N.PA_EFLAG_CTX_OVERFLOW
+    assert np.all(out[:2] == 0) and np.all(np.abs(out[2:]).max(axis=(1, 2)) > 0)
+
+
 def test_prefill_then_decode_over_released_blocks():
     """A stream: chunks and single tokens alternate, blocks leave the pool as the window slides."""
     window, anchors = 50, 4
