@@ -9,7 +9,8 @@
 // Under a sliding window (ldpk §5.3) only the blocks holding the last W positions are listed,
 // so the work, the bytes and the table entries read scale with W, not with the context.  With
 // anchors (pa_decode_attention_anchored) the first tokens stay visible beside the window: their
-// blocks are listed in front of the window's.
+// blocks are listed in front of the window's.  Bound by HBM as without them: 64 sequences of 4096 + 4
+// tokens, 32/8 heads, d 128, bf16, take 165 us (6.5 TB/s, 0.97 of a measured copy; 164 without anchors).
 //
 // Design (GB300, sm_103a):
 //  * Work unit = one 16-token physical block of one head group.  A CTA owns a contiguous range
@@ -1294,7 +1295,9 @@ __global__ void __launch_bounds__(128) merge_kernel(const DecodeParams p, int gr
 // one (sequence, KV head)'s positions, chunks of 128 P of them, and works M and L of its G rows out for
 // itself: a few (m, l) pairs each, all L2 hits, but three dependent round trips, so that there are no
 // more shares than keep the SMs busy.  It runs beside the merge's CTAs in one launch, as both need
-// nothing but the decode kernel.
+// nothing but the decode kernel.  Bound by HBM with the decode kernel (the scores go through L2): 64
+// sequences of 512..4096, 32/8 heads, take 105 us against 91 without weights, 4 of 131072 over an 8-bit
+// cache 207 against 175.
 // ------------------------------------------------------------------------------------
 struct WeightsParams {
   const float* scores_in;  // or null: zeros
