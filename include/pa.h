@@ -517,7 +517,7 @@ pa_status pa_decode_step(const pa_cache_desc* desc, void* out, const void* q, vo
  * A context that is negative, beyond the table or beyond max_context_len sets PA_EFLAG_CTX_OVERFLOW and
  * leaves the sequence as it was, its scores_out and pos_out rows too; a table entry outside
  * [0, num_blocks) under a moved row sets PA_EFLAG_BAD_BLOCK_ID and skips that row's K and V.
- * Every cache kind; desc->sliding_window > 0 gives PA_ERR_UNSUPPORTED.
+ * Every cache kind; desc->sliding_window > 0, or max_context_len > 2097152, gives PA_ERR_UNSUPPORTED.
  * Host errors: PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE_TOO_SMALL, PA_ERR_CUDA. */
 size_t pa_cache_evict_workspace_size(const pa_cache_desc* desc, int max_context_len, int budget);
 
