@@ -49,7 +49,7 @@ namespace {
 constexpr int kEvBins = 4096;
 constexpr int kEvList = 1024;     // keys of the list after the first digit; more: all keys are gone over again
 constexpr int kEvMaxCluster = 8;  // the portable cluster size
-constexpr int kEvSmall = 4096;     // slots up to which a CTA has 256 threads and keeps scores and positions
+constexpr int kEvSmall = 4096;     // slots up to which a CTA keeps scores and positions in shared memory
 constexpr int kEvMaxKeys = 40960;  // keys kept in shared memory otherwise
 constexpr int kEvMaxContext = 1 << 21;  // so that every word of kept bits has its place in shared memory too
 
@@ -665,9 +665,6 @@ extern "C" pa_status pa_cache_evict(const pa_cache_desc* desc, void* k_cache, vo
   while (max_context_len > 16384 && C < pa::kEvMaxCluster && max_context_len / C > 8192 &&
          (max_context_len / C > pa::kEvMaxKeys || pairs * 2 * C <= sms * 5 / 2))
     C *= 2;
-#ifdef PA_EVICT_CLUSTER
-  C = PA_EVICT_CLUSTER;
-#endif
   if (pairs * C > 0x7FFFFFFFLL) return PA_ERR_UNSUPPORTED;
   p.cluster = C;
   const size_t span = std::max<size_t>((static_cast<size_t>((max_context_len + C - 1) / C) + 31) / 32 * 32, 32);
@@ -678,15 +675,18 @@ extern "C" pa_status pa_cache_evict(const pa_cache_desc* desc, void* k_cache, vo
   // threads a CTA, and for 256 with few pairs or many rows.  Inline and apart: 8 pairs from 4096 slots to
   // 2048 25 and 17 us, 64 of them 31 and 25, 400 of them 108 and 97; 400 pairs from 2048 to 1024 47 and 53 us,
   // 64 from 1000 to 900 8.4 and 9.6.
-#ifndef PA_EVICT_APART
-#define PA_EVICT_APART (!small || p.max_moves > (pairs < 3 * sms / 2 ? 256 : 1536))
-#endif
-  p.rows_apart = (PA_EVICT_APART && p.max_moves > 0) ? 1 : 0;
-  auto kern = small ? pa::evict_kernel<256, true> : pa::evict_kernel<512, false>;
+  const int inline_moves = !small ? 0 : (pairs < 3 * sms / 2 ? 256 : 1536);
+  p.rows_apart = p.max_moves > inline_moves ? 1 : 0;
+  // Where each CTA has an SM to itself it takes 1024 threads, from 2048 slots on: 16 pairs of 4096 slots take
+  // 10.8 us with 1024 and 13.6 with 256, of 2048 both 9.2, of 1024 8.4 and 7.0; 128 of 10000 24.2 us and with
+  // 512 24.6; 32 clusters of 32000 27.2 and 26.4.  In two waves they lose: 168 pairs of 1024 15.8 and 7.9.
+  const bool wide = C == 1 && pairs <= sms && max_context_len > 2048;
+  auto kern = small ? (wide ? pa::evict_kernel<1024, true> : pa::evict_kernel<256, true>)
+                    : (wide ? pa::evict_kernel<1024, false> : pa::evict_kernel<512, false>);
   if (!pa::ensure_dynamic_smem(reinterpret_cast<const void*>(kern), key_bytes)) return PA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(pairs * C));
-  cfg.blockDim = dim3(small ? 256 : 512);
+  cfg.blockDim = dim3(wide ? 1024 : (small ? 256 : 512));
   cfg.dynamicSmemBytes = key_bytes;
   cfg.stream = pa::as_stream(stream);
   cudaLaunchAttribute attr[2];

@@ -921,11 +921,7 @@ bool anchored_plan(const pa_cache_desc* d, int max_q, int max_ctx, int anchors, 
     const double copy_bytes = static_cast<double>(d->num_seqs) * span * PA_BLOCK_SIZE * d->num_kv_heads * 768;
     const double rounds = std::ceil(pairs * ((max_q + item - 1) / item) / sms);
     const double tc_us = 9 + 2 * rounds * std::ceil(reach(item) / 8) + (dq ? 5 + copy_bytes / 4.8e6 : 0);
-#ifdef PA_PREFILL_ANCHORED_WARPS
-    pl->warps = PA_PREFILL_ANCHORED_WARPS || !tc;
-#else
     pl->warps = !tc || warps_us < tc_us;
-#endif
     if (pl->warps) {
       pl->splits = splits;
       if (static_cast<long long>(d->num_kv_heads) * splits > 65535) pl->splits = 1;

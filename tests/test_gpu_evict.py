@@ -101,6 +101,16 @@ def test_clusters(n):
     _check(w, [n, 37], n - 1, 0, 1, "ties", given=True)
 
 
+@pytest.mark.parametrize("B", [2, 10])  # 32 pairs, and 160, more than the GPU has SMs
+@pytest.mark.parametrize("n", [2048, 2049, 4096, 4101, 12345])
+def test_threads_of_a_cta(n, B):
+    ctx = [n] + [0, 1, 37, 100, 64, 65, 300, 2, 33][:B - 1]
+    w = workload("bf16", B=B, H_q=16, H_kv=16, D=64, ctx_list=ctx)
+    for mode in ("special", "close"):
+        for budget, anchors, recent in ((n - 1, 4, 16), (n // 2, 0, 0), (33, 4, 1)):
+            _check(w, ctx, budget, anchors, recent, mode, given=mode == "close", in_place=mode == "special")
+
+
 @pytest.mark.parametrize("n,budget", [(500_001, 70_000), (1 << 21, 1 << 20)])
 def test_more_slots_than_shared_memory_holds(n, budget):
     # eight CTAs with 40960 keys each hold 327,680 slots; the rest are ranked from memory
