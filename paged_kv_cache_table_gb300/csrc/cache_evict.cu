@@ -35,7 +35,7 @@
 // Everything is integer comparison and counting in a fixed order: the result does not depend on timing.
 //
 // Measured, d 128 bf16, 8 KV heads: 64 sequences from 2112 slots to 2048 21.5 us (50 MB; bound by the CTA's
-// dependent steps, not by bytes), 16 of 500..8192 to 1024 34.5 us, 4 of 131072 to 32768 188 us (882 MB:
+// dependent steps, not by bytes), 16 of 500..8192 to 1024 30.5 us, 4 of 131072 to 32768 188 us (882 MB:
 // 130 us for the rows at 6.2 TB/s, 50 for the selection).
 
 #include <algorithm>
@@ -671,16 +671,19 @@ extern "C" pa_status pa_cache_evict(const pa_cache_desc* desc, void* k_cache, vo
   const bool small = C == 1 && span <= static_cast<size_t>(pa::kEvSmall);
   p.cap = static_cast<int>(small ? span : std::min<size_t>(span, pa::kEvMaxKeys));
   const size_t key_bytes = static_cast<size_t>(p.cap) * (small ? 8 : 4) + span / 8;
-  // A second launch for the rows when this one has too few warps to keep enough of them in flight: for 512
-  // threads a CTA, and for 256 with few pairs or many rows.  Inline and apart: 8 pairs from 4096 slots to
-  // 2048 25 and 17 us, 64 of them 31 and 25, 400 of them 108 and 97; 400 pairs from 2048 to 1024 47 and 53 us,
-  // 64 from 1000 to 900 8.4 and 9.6.
-  const int inline_moves = !small ? 0 : (pairs < 3 * sms / 2 ? 256 : 1536);
-  p.rows_apart = p.max_moves > inline_moves ? 1 : 0;
   // Where each CTA has an SM to itself it takes 1024 threads, from 2048 slots on: 16 pairs of 4096 slots take
   // 10.8 us with 1024 and 13.6 with 256, of 2048 both 9.2, of 1024 8.4 and 7.0; 128 of 10000 24.2 us and with
   // 512 24.6; 32 clusters of 32000 27.2 and 26.4.  In two waves they lose: 168 pairs of 1024 15.8 and 7.9.
   const bool wide = C == 1 && pairs <= sms && max_context_len > 2048;
+  // A second launch for the rows when this one has too few warps to keep enough of them in flight.  Inline and
+  // apart, 256 threads: 400 pairs from 2048 to 1024 47 and 53 us, from 4096 to 2048 108 and 97, 64 pairs from
+  // 1000 to 900 8.4 and 9.6.  1024 threads: 8 pairs of 4096 slots 10.6 and 11.9 us for 64 moves, 12.0 and 11.5
+  // for 256, 17.8 and 12.0 for 1024; 128 pairs 10.8 and 12.4, 12.4 and 14.0, 23.9 and 27.1.  512 threads lose
+  // inline, and many moves go apart at any number of pairs: they may be all of one long sequence's.
+  const int inline_moves = wide    ? (pairs * 3 > sms * 2 ? 1024 : 256)
+                           : small ? (pairs < 3 * sms / 2 ? 256 : 1536)
+                                   : 0;
+  p.rows_apart = p.max_moves > inline_moves ? 1 : 0;
   auto kern = small ? (wide ? pa::evict_kernel<1024, true> : pa::evict_kernel<256, true>)
                     : (wide ? pa::evict_kernel<1024, false> : pa::evict_kernel<512, false>);
   if (!pa::ensure_dynamic_smem(reinterpret_cast<const void*>(kern), key_bytes)) return PA_ERR_CUDA;
