@@ -167,6 +167,22 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]) : "memory");
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// As tmem_ld32, if `on` (the same on every lane); otherwise v keeps its values.
+__device__ __forceinline__ void tmem_ld32_if(uint32_t on, uint32_t taddr, uint32_t (&v)[32]) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %33, 0;\n\t"
+               "@p tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t}"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+               : "r"(taddr), "r"(on)
+               : "memory");
+}
+// tmem_wait_ld for loads whose registers live on: they are named, so that no copy of one is made before the wait.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[32], uint32_t (&w)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31]),
+                 "+r"(w[0]), "+r"(w[1]), "+r"(w[2]), "+r"(w[3]), "+r"(w[4]), "+r"(w[5]), "+r"(w[6]), "+r"(w[7]), "+r"(w[8]), "+r"(w[9]), "+r"(w[10]), "+r"(w[11]), "+r"(w[12]), "+r"(w[13]), "+r"(w[14]), "+r"(w[15]), "+r"(w[16]), "+r"(w[17]), "+r"(w[18]), "+r"(w[19]), "+r"(w[20]), "+r"(w[21]), "+r"(w[22]), "+r"(w[23]), "+r"(w[24]), "+r"(w[25]), "+r"(w[26]), "+r"(w[27]), "+r"(w[28]), "+r"(w[29]), "+r"(w[30]), "+r"(w[31])
+               :
+               : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // A wait that every lane of the warp leaves with the same answer.
@@ -188,6 +204,20 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// Two fp32 operations in one instruction: (a, b) * s + c, and (s, t) += (a, b).
+__device__ __forceinline__ void fma_pair(uint32_t a, uint32_t b, float s, float c, float* x, float* y) {
+  asm("{\n\t.reg .b64 v, s, c;\n\tmov.b64 v, {%2, %3};\n\tmov.b64 s, {%4, %4};\n\tmov.b64 c, {%5, %5};\n\t"
+      "fma.rn.f32x2 v, v, s, c;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "=f"(*x), "=f"(*y)
+      : "r"(a), "r"(b), "f"(s), "f"(c));
+}
+__device__ __forceinline__ void add_pair(float& s, float& t, float a, float b) {
+  asm("{\n\t.reg .b64 v, w;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 w, {%2, %3};\n\tadd.rn.f32x2 v, v, w;\n\t"
+      "mov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(s), "+f"(t)
+      : "f"(a), "f"(b));
 }
 
 // A 4-D TMA box into this CTA's shared memory, completion counted on `bar`.
@@ -322,7 +352,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* o_done = bars + 18;  // [2]
   uint64_t* drain = bars + 20;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 21);
-  int* flags = reinterpret_cast<int*>(bars + 22);  // [0] tiles of all sequences, [1] a wait gave up, [2..3] score scales
+  int* flags = reinterpret_cast<int*>(bars + 22);  // [0] tiles of all sequences, [1] a wait gave up
   ItemRec* list = reinterpret_cast<ItemRec*>(sm + kListOff);  // this CTA's items, in order
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -664,13 +694,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int row_lo = p.window > 0 ? max(0, row_pos - p.window + 1) : 0;
       const int kbase0 = (it.kb0 - (ANCH ? it.ab : 0)) * PA_BLOCK_SIZE;  // position of list column 0, window part
       float m_run = kNegInfTc, l_run = 0.f;
-      // FOLD: the score scale of this KV head goes through shared memory, read again at each use: held in a
-      // register across the tile loop it costs the loop twice its time (the scores take 128 of 168)
-      volatile float* head_scale = reinterpret_cast<volatile float*>(flags + 2) + wg;
-      if constexpr (FOLD) {
-        if (r == 0) *head_scale = p.scale_log2 * folded_scale(p.k_scales[it.h_kv]);
-        group_sync(1 + wg);  // (its readers of the item before have met at that item's output)
-      }
+      const float sl = FOLD ? p.scale_log2 * folded_scale(p.k_scales[it.h_kv]) : p.scale_log2;
       for (int k = 0; ok && k < nt; ++k) {
         if (!warp_wait(&s_full[wg], sp & 1u)) {
           ok = false;
@@ -678,44 +702,56 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         ++sp;
         tc_fence_after();
-        uint32_t sv[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * c));
-        tmem_wait_ld();
         const int kbase = kbase0 + 128 * k;
         // scores stay raw (the scale is positive, so the maximum commutes with it); only tiles
         // that cross a row's causal or window edge take the per-key mask, and within them only
-        // the 32-key chunks that some row of the warp attends in part (a row attends the tile's
-        // columns lo .. hi; on a diagonal tile a warp's rows, 32 / G tokens, put one or two of
-        // the four chunks across their edges).  A chunk that no row of the warp attends (`dead`,
-        // the keys past the item's last query on its diagonal tile) takes no maximum and no
-        // exponentials: its P is zero.
-        unsigned dead = 0;
+        // the 32-key chunks that some row of the warp attends in part.  The masked chunks go back to
+        // TMEM, so that one unrolled chunk of mask code serves all four: the tile loop has to
+        // stay small (see below).
         if (!__all_sync(0xffffffffu, row_ok && kbase + 127 <= row_pos && kbase >= row_lo)) {
-          const int lo = row_lo - kbase, hi = row_ok ? row_pos - kbase : -1;
-          const int an = ANCH ? p.anchors - 128 * k : 0;  // columns below it are anchors, attended up to hi
-#pragma unroll
+          auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };  // columns < n
+#pragma unroll 1
           for (int q = 0; q < 4; ++q) {
-            if (__all_sync(0xffffffffu, hi >= 32 * q + 31 && (lo <= 32 * q || an >= 32 * q + 32))) continue;
-            if (__all_sync(0xffffffffu, hi < 32 * q || (lo > 32 * q + 31 && an <= 32 * q))) {
-              dead |= 1u << q;
-              continue;
-            }
+            const int c0 = kbase + 32 * q;
+            uint32_t hide = below(row_lo - c0);
+            if constexpr (ANCH) hide &= ~below(p.anchors - 128 * k - 32 * q);  // anchors
+            const uint32_t keep = row_ok ? below(row_pos - c0 + 1) & ~hide : 0u;
+            if (__all_sync(0xffffffffu, keep == ~0u)) continue;
+            uint32_t v[32];
+            tmem_ld32(tS + 32 * q, v);
+            tmem_wait_ld();
 #pragma unroll
-            for (int c = 32 * q; c < 32 * q + 32; ++c)
-              if (c > hi || (c < lo && !(ANCH && c < an))) sv[c] = __float_as_uint(kNegInfTc);
+            for (int c = 0; c < 32; ++c)
+              if (!(keep >> c & 1u)) v[c] = __float_as_uint(kNegInfTc);
+            tmem_st32(tS + 32 * q, v);
           }
+          tmem_wait_st();
         }
+        // the row's maximum; keys 0-63, which the exponentials start with, stay in registers
         float mx4[4] = {kNegInfTc, kNegInfTc, kNegInfTc, kNegInfTc};
+        auto chunk_max = [&](const uint32_t (&v)[32], int j) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if ((dead >> q) & 1u) continue;
-#pragma unroll
-          for (int c = 32 * q; c < 32 * q + 32; c += 2)
-            mx4[(c >> 1) & 3] = max3f(mx4[(c >> 1) & 3], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+          for (int c = 0; c < 32; c += 2) {
+            float& m = mx4[j + ((c >> 1) & 1)];
+            m = max3f(m, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+          }
+        };
+        uint32_t va[32], vb[32];
+        {
+          uint32_t vc[32], vd[32];
+          tmem_ld32(tS + 64, vc);
+          tmem_ld32(tS + 96, vd);
+          tmem_wait_ld(vc, vd);
+          tmem_ld32(tS, va);
+          tmem_ld32(tS + 32, vb);
+          chunk_max(vc, 0);
+          chunk_max(vd, 2);
+          tmem_wait_ld(va, vb);
+          chunk_max(va, 0);
+          chunk_max(vb, 2);
         }
         const float mraw = fmaxf(max3f(mx4[0], mx4[1], mx4[2]), mx4[3]);
-        const float mx = mraw == kNegInfTc ? kNegInfTc : mraw * (FOLD ? *head_scale : p.scale_log2);
+        const float mx = mraw == kNegInfTc ? kNegInfTc : mraw * sl;
         const float m_new = (m_run == kNegInfTc || mx > m_run + 8.f) ? fmaxf(m_run, mx) : m_run;
         const float ms = m_new == kNegInfTc ? 0.f : m_new;
         const float alpha = ex2(m_run - ms);
@@ -742,31 +778,39 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           fence_proxy_async();  // the zeros, before the tensor core reads the stage
         }
-        // P (bf16 pairs) over the S columns just read: column c holds keys 2c and 2c + 1; when the
-        // maximum moved, O is rescaled before P is handed over.
+        // P (bf16 pairs) over S columns that have been read: column c holds keys 2c and 2c + 1; when the
+        // maximum moved, O is rescaled before P is handed over.  Two chunks of 32 keys are unrolled and
+        // gone through twice, the second two loaded meanwhile: with all 128 scores in registers and
+        // everything unrolled the loop outgrows the instruction cache and spills (8 x 512 queries over
+        // 4096 keys 255 us, now 227; 6 chunks of up to 700 over 1000 128 us, now 113).
         float ls4[4] = {0.f, 0.f, 0.f, 0.f};
-        const float sl = FOLD ? *head_scale : p.scale_log2;
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {  // a quarter (32 keys, 16 columns) at a time
+        auto chunk_exp = [&](const uint32_t (&v)[32], int h) {
           uint32_t pw[16];
-          if ((dead >> h) & 1u) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) pw[e] = 0u;
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float a = ex2(fmaf(__uint_as_float(sv[32 * h + 2 * e]), sl, -ms));
-              const float b = ex2(fmaf(__uint_as_float(sv[32 * h + 2 * e + 1]), sl, -ms));
-              ls4[e & 3] += a + b;
-              pw[e] = pack_bf16(a, b);
-            }
+          for (int e = 0; e < 16; ++e) {
+            float a, b;
+            fma_pair(v[2 * e], v[2 * e + 1], sl, -ms, &a, &b);
+            a = ex2(a);
+            b = ex2(b);
+            if constexpr (ANCH) add_pair(ls4[2 * (e & 1)], ls4[2 * (e & 1) + 1], a, b);
+            else ls4[e & 3] += a + b;
+            pw[e] = pack_bf16(a, b);
           }
           tmem_st16(tS + 16 * h, pw);
+        };
+#pragma unroll 1
+        for (int h = 0; h < 4; h += 2) {
+          const uint32_t more = h == 0;
+          chunk_exp(va, h);
+          tmem_ld32_if(more, tS + 64, va);
+          chunk_exp(vb, h + 1);
+          tmem_ld32_if(more, tS + 96, vb);
+          tmem_wait_ld(va, vb);
         }
         tmem_wait_st();
         l_run = l_run * alpha + ((ls4[0] + ls4[1]) + (ls4[2] + ls4[3]));
         if (moved) {
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t ov[32];
             tmem_ld32(tO + 32 * c, ov);
