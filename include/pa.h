@@ -418,8 +418,9 @@ pa_status pa_prefill_step_ws(const pa_cache_desc* desc, void* out, const void* q
  *                     (8-bit, per-token-scaled, INT4, with sinks) are decoded into it block by block,
  *                     once, as by pa_prefill_attention_ws, but only the blocks that the chunk can
  *                     attend, so its size goes with W + max_query_len + num_anchor, not with the
- *                     context.  With few rows the keys of a query tile are split over several CTAs,
- *                     and it takes their partial rows.  The size is 0 when the call needs none
+ *                     context.  Where the query tiles do not fill the GPU, the keys of a tile are
+ *                     split over several CTAs, and it takes their partial rows: which tiles are split
+ *                     depends on the whole batch, and so do a sequence's last bits.  The size is 0 when the call needs none
  *                     (workspace may then be NULL) or an argument is invalid; ask for it on the
  *                     device that the call runs on.  With anchors and a window, 8-bit caches with
  *                     per-head scales keep their bare codes there (the scales multiply the scores and

@@ -181,6 +181,23 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// pa_prefill_attention_anchored: `items` tcgen05 work items of about `tiles` key tiles are left for one round of
+// `ctas` CTAs that they do not fill.  The parts (1 to 8, together at most two rounds) that each is cut into, by
+// the time in microseconds that this takes (*us): 1.75 per tile, 2.5 per part, 4 for writing parts and joining.
+__host__ __device__ inline int prefill_parts(int items, int ctas, int tiles, float* us = nullptr) {
+  int best = 1;
+  float least = items > 0 ? 1.75f * tiles + 2.5f : 0.f;
+  for (int s = 2; s <= 8 && items > 0 && items * s <= 2 * ctas; ++s) {
+    const float t = (items * s + ctas - 1) / ctas * (1.75f * ((tiles + s - 1) / s) + 2.5f) + 4.f;
+    if (t < least) {
+      least = t;
+      best = s;
+    }
+  }
+  if (us) *us = least;
+  return best;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);

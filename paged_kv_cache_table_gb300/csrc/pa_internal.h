@@ -78,14 +78,24 @@ bool ensure_dynamic_smem(const void* kernel, size_t bytes);
 // query heads per KV head; arguments as pa_prefill_attention after its checks.
 // step: the previous kernel on the stream is the append of this prefill step (it writes only
 // K/V slots), so only the K/V copies wait for it.
-// anchors: positions below it stay visible beside the sliding window (0: none).
-// k_scales, v_scales (anchors > 0 and a window only): K and V hold values divided by these scales per KV
-// head (folded_scale of each), which the kernel applies to the scores and the output.
+// What pa_prefill_attention_anchored adds (with anchors > 0 and a window; else the defaults).
+struct AnchoredPrefill {
+  int anchors = 0;             // positions below it stay visible beside the window
+  int max_ctx = 0x7FFFFFFF;    // contexts beyond it are invalid
+  // K and V hold values divided by these scales per KV head (folded_scale of each), which the kernel applies
+  // to the scores and the output
+  const float* k_scales = nullptr;
+  const float* v_scales = nullptr;
+  // workspace of prefill_parts_bytes(items, part_ctas) for cutting the last round's items, of about `tiles` key
+  // tiles, in parts; part_ctas CTAs are launched, items is at most 32 times that (null: items stay whole)
+  void* parts = nullptr;
+  int part_ctas = 0, tiles = 0;
+};
 pa_status launch_prefill_tc(const pa_cache_desc* desc, void* out, const void* q, const void* k_cache,
                             const void* v_cache, const int32_t* block_tables, const int32_t* q_start,
                             const int32_t* context_lens, int max_query_len, float scale, int32_t* err_flag,
-                            cudaStream_t stream, bool step, int anchors = 0, const float* k_scales = nullptr,
-                            const float* v_scales = nullptr);
+                            cudaStream_t stream, bool step, const AnchoredPrefill& a = {});
+size_t prefill_parts_bytes(long long items, int ctas);
 
 // Shared-prefix decode (shared_prefix.cu).  Per-sequence flags, zeroed then or-ed by the prefix
 // kernel: kSharedMember = listed, in range, context covering the prefix; kSharedMismatch = some

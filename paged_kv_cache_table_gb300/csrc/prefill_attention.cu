@@ -824,17 +824,17 @@ pa_status prefill_warps(const pa_cache_desc* desc, const PrefillParams& p, const
 pa_status prefill_launch(const pa_cache_desc* desc, void* out, const void* q, const void* k_cache,
                          const void* v_cache, const int32_t* block_tables, const int32_t* q_start,
                          const int32_t* context_lens, int max_query_len, float scale, int32_t* err_flag,
-                         void* stream, bool step, int anchors = 0) {
+                         void* stream, bool step, const AnchoredPrefill& a = {}) {
   const int G = desc->num_q_heads / desc->num_kv_heads;
   const bool dq = is_quantized(desc) || desc->num_sink > 0;
 #ifndef PA_PREFILL_WARP_MMA_ONLY
   if (!dq && desc->head_dim == 128 && (G & (G - 1)) == 0)  // the tensor-core (tcgen05) kernel
     return launch_prefill_tc(desc, out, q, k_cache, v_cache, block_tables, q_start, context_lens, max_query_len,
-                             scale, err_flag, as_stream(stream), step, anchors);
+                             scale, err_flag, as_stream(stream), step, a);
 #endif
   (void)step;  // the warp-MMA kernel waits for its predecessor before it starts
   return prefill_warps(desc, prefill_params(desc, out, q, k_cache, v_cache, block_tables, q_start, context_lens,
-                                            max_query_len, scale, err_flag, anchors), k_cache, v_cache, stream);
+                                            max_query_len, scale, err_flag, a.anchors), k_cache, v_cache, stream);
 }
 
 // Bytes of pa_prefill_attention_ws's workspace (and the bf16 pool's blocks per sequence in *mb):
@@ -866,17 +866,21 @@ size_t prefill_ws_bytes(const pa_cache_desc* d, int max_ctx, int* mb_out) {
 struct AnchoredPlan {
   bool warps, expand;
   int mb, cap, splits;
-  size_t bytes;  // workspace
+  int part_ctas, tiles;  // tensor-core kernel with the last round's items in parts: its CTAs (0: no parts), tiles of an item
+  size_t parts;          // the parts' offset in the workspace
+  size_t bytes;          // workspace
 };
 
-// The choice goes by the time that either takes, in microseconds, fitted to 108 shapes (1 to 16 sequences,
-// chunks of 1 to 512 tokens, windows of 64 to 4096, 1, 4 and 8 query heads per KV head; mean error 10 %):
+// The choice goes by the time that either takes, in microseconds, fitted to measured shapes (1 to 16 sequences,
+// chunks of 1 to 512 tokens, windows of 64 to 4096, 1, 4 and 8 query heads per KV head; mean errors 11 and 9 %):
 //   warp-MMA  6, and 3 for the join; per block of a CTA's share 0.04 by TMA, 0.45 decoded; per block of all
 //             CTAs over the SMs 0.45 and 0.54.  A CTA has 4 x 16 / G query tokens;
-//   tcgen05   9, and 2 per tile of 8 blocks of an SM's items of 256 query rows; the decoded copy 5 and its
-//             bytes at 4.8 TB/s.
-// One sequence's chunk of 8 tokens over a window of 4096, 32/8 heads: 18 against 71; 16 sequences' chunks of
-// 32: 233 against 70.
+//   tcgen05   9; 2.5 per item of 256 query rows of an SM and 1.75 per tile of 8 blocks, 0.5 more when no other
+//             item brings the tile to L2, the last round's items in parts (prefill_parts); the decoded copy 5
+//             and its bytes at 4.8 TB/s.
+// One sequence's chunk of 8 tokens over a window of 4096, 32/8 heads: 21 against 29; of 64: 34 against 27 (66 with
+// whole items); 16 sequences' chunks of 32: 225 against 66.  Of 336 shapes 6 lose more than 8 % to the other side,
+// the worst 16 %.
 bool anchored_plan(const pa_cache_desc* d, int max_q, int max_ctx, int anchors, AnchoredPlan* pl) {
   if (validate_desc(d) != PA_OK || max_q < 0 || anchors < 0 || max_ctx < 0 ||
       static_cast<long long>(max_ctx) > static_cast<long long>(d->max_blocks_per_seq) * PA_BLOCK_SIZE)
@@ -919,8 +923,26 @@ bool anchored_plan(const pa_cache_desc* d, int max_q, int max_ctx, int anchors, 
     const double warps_us = 6 + (splits > 1 ? 3 : 0) + (dq ? 0.45 : 0.04) * std::ceil(blocks / splits) +
                             (dq ? 0.54 : 0.45) * ctas * blocks / sms;
     const double copy_bytes = static_cast<double>(d->num_seqs) * span * PA_BLOCK_SIZE * d->num_kv_heads * 768;
-    const double rounds = std::ceil(pairs * ((max_q + item - 1) / item) / sms);
-    const double tc_us = 9 + 2 * rounds * std::ceil(reach(item) / 8) + (dq ? 5 + copy_bytes / 4.8e6 : 0);
+    const double items = pairs * ((max_q + item - 1) / item);
+    pl->tiles = static_cast<int>(std::ceil(reach(item) / 8));
+    // parts: where an item is long enough to be cut and a round of the grid counts.  The kernel chooses by the
+    // chunks that it finds; one sequence's is known here (a join with nothing to do costs 2 us)
+    float last_us = 2.5f + 1.75f * static_cast<float>(pl->tiles);
+    double rounds = std::ceil(items / sms) - 1, last_tiles = pl->tiles;
+    if (tc && pl->tiles >= 8 && items <= 8.0 * sms) {
+      const int last = static_cast<int>(items) % sms;
+      float us;
+      const int parts = prefill_parts(last, sms, pl->tiles, &us);
+      if (parts > 1) {
+        rounds = std::floor(items / sms);
+        last_us = us;
+        last_tiles = (last * parts + sms - 1) / sms * ((pl->tiles + parts - 1) / parts);
+      }
+      if (parts > 1 || d->num_seqs > 1) pl->part_ctas = sms;
+    }
+    const double tc_us = 9 + rounds * (2.5 + 1.75 * pl->tiles) + last_us +
+                         (max_q <= item ? 0.5 * (rounds * pl->tiles + last_tiles) : 0) +
+                         (dq ? 5 + copy_bytes / 4.8e6 : 0);
     pl->warps = !tc || warps_us < tc_us;
     if (pl->warps) {
       pl->splits = splits;
@@ -929,12 +951,18 @@ bool anchored_plan(const pa_cache_desc* d, int max_q, int max_ctx, int anchors, 
   }
   if (pl->warps) {
     pl->expand = false;
+    pl->part_ctas = 0;
     pl->bytes = pl->splits == 1 ? 0
                                 : static_cast<size_t>(d->num_seqs) * max_q * d->num_q_heads * pl->splits *
                                       (d->head_dim + 4) * sizeof(float);
   } else if (pl->expand) {
     const size_t table = (static_cast<size_t>(d->num_seqs) * pl->mb * 4 + 255) / 256 * 256;
     pl->bytes = table + 2 * (static_cast<size_t>(d->num_seqs) * cap * PA_BLOCK_SIZE * d->num_kv_heads * 128 * 2);
+  }
+  if (pl->part_ctas > 0) {
+    pl->parts = pl->bytes;  // a multiple of 256
+    pl->bytes += prefill_parts_bytes(static_cast<long long>(d->num_seqs) * d->num_kv_heads *
+                                         ((max_q + 256 / G - 1) / (256 / G)), pl->part_ctas);
   }
   return true;
 }
@@ -945,9 +973,9 @@ bool anchored_plan(const pa_cache_desc* d, int max_q, int max_ctx, int anchors, 
 pa_status prefill_expanded(const pa_cache_desc* desc, void* out, const void* q, const void* k_cache,
                            const void* v_cache, const int32_t* block_tables, const int32_t* q_start,
                            const int32_t* context_lens, int max_query_len, float scale, int mb, void* workspace,
-                           int32_t* err_flag, void* stream, int cap = 0, int anchors = 0) {
+                           int32_t* err_flag, void* stream, int cap = 0, AnchoredPrefill a = {}) {
   const PrefillParams p = prefill_params(desc, out, q, k_cache, v_cache, block_tables, q_start, context_lens,
-                                         max_query_len, scale, err_flag, anchors);
+                                         max_query_len, scale, err_flag, a.anchors);
   const int per_seq = cap > 0 ? cap : mb;
   const size_t table = (static_cast<size_t>(desc->num_seqs) * mb * 4 + 255) / 256 * 256;
   const size_t pool = static_cast<size_t>(desc->num_seqs) * per_seq * PA_BLOCK_SIZE * desc->num_kv_heads * 128 * 2;
@@ -955,7 +983,7 @@ pa_status prefill_expanded(const pa_cache_desc* desc, void* out, const void* q, 
   auto* kx = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(workspace) + table);
   auto* vx = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(workspace) + table + pool);
   // per-head scales are applied by the attention kernel of the anchored call
-  const bool fold = cap > 0 && anchors > 0 && desc->sliding_window > 0 && desc->k_dtype == PA_FP8_E4M3;
+  const bool fold = cap > 0 && a.anchors > 0 && desc->sliding_window > 0 && desc->k_dtype == PA_FP8_E4M3;
   cudaStream_t s = as_stream(stream);
   const dim3 grid(per_seq, desc->num_seqs), block(256);
   pa_status st;
@@ -973,8 +1001,12 @@ pa_status prefill_expanded(const pa_cache_desc* desc, void* out, const void* q, 
   x.num_sink = 0;
   x.num_blocks = desc->num_seqs * per_seq;
   x.max_blocks_per_seq = mb;
+  if (fold) {
+    a.k_scales = desc->k_scales;
+    a.v_scales = desc->v_scales;
+  }
   return launch_prefill_tc(&x, out, q, kx, vx, dense, q_start, context_lens, max_query_len, scale, err_flag, s,
-                           false, anchors, fold ? desc->k_scales : nullptr, fold ? desc->v_scales : nullptr);
+                           false, a);
 }
 }  // namespace
 }  // namespace pa
@@ -1050,11 +1082,19 @@ extern "C" pa_status pa_prefill_attention_anchored(const pa_cache_desc* desc, vo
     }
     return pa::prefill_warps(desc, p, k_cache, v_cache, stream);
   }
+  pa::AnchoredPrefill a;
+  a.anchors = anchors;
+  if (pl.bytes > 0) a.max_ctx = max_context_len;
+  if (pl.part_ctas > 0) {
+    a.parts = static_cast<uint8_t*>(workspace) + pl.parts;
+    a.part_ctas = pl.part_ctas;
+    a.tiles = pl.tiles;
+  }
   if (!pl.expand)
     return pa::prefill_launch(desc, out, q, k_cache, v_cache, block_tables, q_start, context_lens, max_query_len,
-                              scale, err_flag, stream, false, anchors);
+                              scale, err_flag, stream, false, a);
   return pa::prefill_expanded(desc, out, q, k_cache, v_cache, block_tables, q_start, context_lens, max_query_len,
-                              scale, pl.mb, workspace, err_flag, stream, pl.cap, anchors);
+                              scale, pl.mb, workspace, err_flag, stream, pl.cap, a);
 }
 
 extern "C" pa_status pa_prefill_step_ws(const pa_cache_desc* desc, void* out, const void* q, void* k_cache,

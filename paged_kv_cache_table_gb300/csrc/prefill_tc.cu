@@ -52,6 +52,12 @@
 //    anchors cost one block, not a tile of their own.  In a tile, key column c is an anchor iff
 //    c < A - 128k (the list starts at position 0), and the window's columns are at
 //    (kb0 - ab + 8k) 16 + c, so a row's mask is two intervals: [0, A - 128k) and [lo, hi].
+//  * Parts (ANCH, with a workspace).  A CTA walks its item's keys alone, about 1.75 us per tile, so a few items
+//    over a long window, or a last round that does not fill the grid, leave most SMs idle.  The items of that
+//    round are cut into up to 8 parts along their key tiles (prefill_parts weighs the shorter walk against more
+//    rounds and the join); a part leaves its rows' O, maximum and sum in the workspace (fp32: they are summed
+//    again) and prefill_parts_kernel joins them.  One chunk of 256 tokens over 4096 keys, 32/8 heads: 67 -> 33 us;
+//    of 512: 67 -> 46; 8 x 512: 254 -> 233; a launch that finds nothing to join costs 2.
 //  * Output: O / l as bf16 is staged in the idle ring stage of the item's last tile (K for query
 //    tile 0, V for query tile 1) and stored by TMA; the stage is then released to its copy warp.
 //    Only a tile holding rows past its sequence is stored row by row.
@@ -95,6 +101,7 @@ constexpr uint32_t kIdescPV = kIdescS | (1u << 16);
 struct TcParams {
   int B, H_q, H_kv, G, num_blocks, max_blocks, max_q, window;
   int anchors;  // positions below it stay visible beside the window (ANCH)
+  int max_ctx;  // contexts beyond it are invalid
   // FOLD, K and V of an 8-bit cache as bare codes: their scales per KV head, which multiply the scores
   // and the output (as folded_scale of each)
   const float* k_scales;
@@ -108,7 +115,17 @@ struct TcParams {
   const __nv_bfloat16* q;
   __nv_bfloat16* out;
   int32_t* err;
+  // ANCH: items in parts (see prefill_parts; null: none).  Header {items in parts, parts}, the items as
+  // {sequence, tile, KV head, 0}, and per part and query tile O as float4 [32][128 rows], then {m, l} [128]; l < 0:
+  // a row of an item with a bad block id.
+  int2* split;
+  int tiles;  // key tiles of an item, for the choice of parts
 };
+constexpr int kPartTile = 128 * (128 + 2);  // floats of a part's query tile
+__host__ __device__ __forceinline__ size_t part_items_off() { return 256; }
+__host__ __device__ __forceinline__ size_t part_data_off(int ctas) {
+  return part_items_off() + (static_cast<size_t>(ctas) * 16 + 255) / 256 * 256;
+}
 
 // Shared-memory operand descriptor, 128-byte swizzle: start address (bits 0-13), leading and
 // stride byte offsets (bits 16-29, 32-45; all encoded >> 4), the fixed 0b001 of bits 46-48, and
@@ -252,7 +269,7 @@ constexpr int kMaxOrderSeqs = 2 * kTile / static_cast<int>(sizeof(SeqGeo));  // 
 __device__ __forceinline__ SeqGeo seq_geo(const TcParams& p, int s, int lw) {
   const int n = p.q_start[s + 1] - p.q_start[s], ctx = p.context_lens[s];
   SeqGeo g;
-  g.valid = n >= 0 && n <= ctx && n <= p.max_q && ctx <= p.max_blocks * PA_BLOCK_SIZE;
+  g.valid = n >= 0 && n <= ctx && n <= p.max_q && ctx <= p.max_blocks * PA_BLOCK_SIZE && ctx <= p.max_ctx;
   g.n = g.valid ? n : min(max(n, 0), p.max_q);
   g.fp = ctx - n;
   g.nc = (g.n + (1 << lw) - 1) >> lw;
@@ -271,25 +288,27 @@ __device__ __forceinline__ int count_ge(const SeqGeo& g, int X, int lw) {
 // t0 = c tpc, tpc = 2 tpq tokens per tile) against KV head h_kv, in two query tiles of tpq tokens;
 // the CTA reads the keys [kv_lo, kv_end), blocks [kb0, kb_end), in n_tiles tiles of 8 blocks.  With
 // anchors its n_list blocks are [0, ab), then [kb0, kb_end); ab = 0 when the anchors' blocks reach
-// kb0, which is then 0 (the list is one run).
+// kb0, which is then 0 (the list is one run).  A part of an item reads n_tiles tiles from the k0-th.
 struct Item {
-  int s, h_kv, tile, qs, n, t0, t_end, first_pos, kv_lo, kb0, kb_end, ab, n_list, n_tiles, loaded_end;
+  int s, h_kv, tile, qs, n, t0, t_end, first_pos, kv_lo, kb0, kb_end, ab, n_list, k0, n_tiles, loaded_end;
   bool valid, has0, has1;
   __device__ __forceinline__ int block(int b) const { return b < ab ? b : kb0 + b - ab; }  // of list entry b
 };
 // An entry of a CTA's item list (shared memory): the sequence, the tile and KV head
 // (c << 16 | h), and the sequence's first query row, query rows and context length.
+// part: 0 the whole item, else (index << 8 | parts << 4 | j), the j-th of 2 to 8 parts of its key tiles; index
+// counts the items that are in parts.
 struct ItemRec {
-  int s, ch, qs, n, ctx, pad;
+  int s, ch, qs, n, ctx, part;
 };
-__device__ __forceinline__ ItemRec item_rec(const TcParams& p, int s, int c, int h) {
+__device__ __forceinline__ ItemRec item_rec(const TcParams& p, int s, int c, int h, int part = 0) {
   ItemRec e;
   e.s = s;
   e.ch = (c << 16) | h;
   e.qs = p.q_start[s];
   e.n = p.q_start[s + 1] - e.qs;
   e.ctx = p.context_lens[s];
-  e.pad = 0;
+  e.part = part;
   return e;
 }
 template <bool ANCH>
@@ -302,13 +321,13 @@ __device__ __forceinline__ Item make_item(const TcParams& p, const ItemRec& e) {
   it.qs = e.qs;
   it.n = e.n;
   const int ctx = e.ctx;
-  it.valid = it.n >= 0 && it.n <= ctx && it.n <= p.max_q && ctx <= p.max_blocks * PA_BLOCK_SIZE;
+  it.valid = it.n >= 0 && it.n <= ctx && it.n <= p.max_q && ctx <= p.max_blocks * PA_BLOCK_SIZE && ctx <= p.max_ctx;
   it.t0 = it.tile * tpc;
   it.has0 = it.valid && it.t0 < it.n;
   it.has1 = it.valid && it.t0 + p.tpq < it.n;
   it.first_pos = ctx - it.n;
   it.t_end = min(it.n, it.t0 + tpc);
-  it.kv_lo = it.kb0 = it.kb_end = it.ab = it.n_list = it.n_tiles = it.loaded_end = 0;
+  it.kv_lo = it.kb0 = it.kb_end = it.ab = it.n_list = it.k0 = it.n_tiles = it.loaded_end = 0;
   if (it.has0) {
     const int kv_end = it.first_pos + it.t_end;
     it.kv_lo = p.window > 0 ? max(0, it.first_pos + it.t0 - p.window + 1) : 0;
@@ -321,6 +340,11 @@ __device__ __forceinline__ Item make_item(const TcParams& p, const ItemRec& e) {
     }
     it.n_list = it.ab + it.kb_end - it.kb0;
     it.n_tiles = (it.n_list + 7) / 8;
+    if (ANCH && e.part) {
+      const int parts = e.part >> 4 & 15, per = (it.n_tiles + parts - 1) / parts;
+      it.k0 = min(it.n_tiles, (e.part & 15) * per);
+      it.n_tiles = min(per, it.n_tiles - it.k0);
+    }
     it.loaded_end = min(ctx, it.kb_end * PA_BLOCK_SIZE);  // keys past this hold no loaded data
   }
   return it;
@@ -352,7 +376,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* o_done = bars + 18;  // [2]
   uint64_t* drain = bars + 20;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 21);
-  int* flags = reinterpret_cast<int*>(bars + 22);  // [0] tiles of all sequences, [1] a wait gave up
+  // [0] tiles of all sequences, [1] a wait gave up, [2..3] a bit per listed item: a table entry outside the pool
+  int* flags = reinterpret_cast<int*>(bars + 22);
   ItemRec* list = reinterpret_cast<ItemRec*>(sm + kListOff);  // this CTA's items, in order
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -380,7 +405,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&o_done[i], 1);
     }
     mbar_init(drain, 1);
-    flags[0] = flags[1] = 0;
+    flags[0] = flags[1] = flags[2] = flags[3] = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -407,7 +432,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // Work items longest first: item (s, c) of key k sits at rank = #items of larger key + #items of
   // key k in earlier sequences; with KV heads innermost, launch position = rank * H_kv + h.
   // Many sequences: last tiles first, sequences in order (slots past a sequence are empty).
-  const int p_tot = lpt ? flags[0] * p.H_kv : p.B * nclx * p.H_kv;
+  const int p_all = lpt ? flags[0] * p.H_kv : p.B * nclx * p.H_kv;
+  // ANCH: the items of the last, unfilled round may be cut in parts (positions from `whole` on count that often)
+  int whole = p_all, parts = 1;
+  if constexpr (ANCH) {
+    if (p.split) {
+      if (lpt) parts = prefill_parts(p_all % NC, NC, p.tiles);
+      if (parts > 1) whole = p_all - p_all % NC;
+      if (cid == 0 && tid == 0) p.split[0] = make_int2(p_all - whole, parts);
+    }
+  }
+  const int p_tot = whole + (p_all - whole) * parts;
   const int rounds = (p_tot + NC - 1) / NC;
   const int n_items = min(kMaxItems, rounds == 0 ? 0 : rounds - 1 + (round_pos(rounds - 1, NC, cid) < p_tot ? 1 : 0));
   if (lpt) {
@@ -423,8 +458,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         rk += above + (q < s ? count_ge(gq, key, lw) - above : 0);
       }
       for (int h = 0; h < p.H_kv; ++h) {
-        const int pos = rk * p.H_kv + h, r = pos / NC, w = pos - r * NC;
-        if (((r & 1) ? NC - 1 - w : w) == cid && r < kMaxItems) list[r] = item_rec(p, s, c, h);
+        const int pos = rk * p.H_kv + h;
+        const bool cut = ANCH && pos >= whole;
+        if (cut && cid == 0)
+          reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(p.split) + part_items_off())[pos - whole] = make_int4(s, c, h, 0);
+        for (int j = 0; j < (cut ? parts : 1); ++j) {
+          const int at = cut ? whole + (pos - whole) * parts + j : pos, r = at / NC, w = at - r * NC;
+          if (((r & 1) ? NC - 1 - w : w) == cid && r < kMaxItems)
+            list[r] = item_rec(p, s, c, h, cut ? (pos - whole) << 8 | parts << 4 | j : 0);
+        }
       }
     }
   } else {
@@ -480,7 +522,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // chunks c0, c0 + 1 and c0 + 2: the accesses only move forward, so a chunk is loaded two
       // chunks before it is first needed and its latency is hidden.
       auto entry = [&](int c) { const int b = 32 * c + lane; return b < it.n_list ? row[it.block(b)] : -1; };
-      int c0 = 0, e0 = entry(0), e1 = entry(1), e2 = entry(2);
+      int c0 = it.k0 / 4, e0 = entry(c0), e1 = entry(c0 + 1), e2 = entry(c0 + 2);
       auto table = [&](int b) -> int {  // entry of list block b; b is in the same chunk on every lane
         const int cb = __shfl_sync(0xffffffffu, b, 0) >> 5;
         while (cb > c0 + 1) {
@@ -492,13 +534,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int v0 = __shfl_sync(0xffffffffu, e0, b & 31), v1 = __shfl_sync(0xffffffffu, e1, b & 31);
         return cb == c0 ? v0 : v1;
       };
-      for (int k = 0; ok && k < it.n_tiles; ++k) {
+      for (int k = it.k0; ok && k < it.k0 + it.n_tiles; ++k) {
         const int ent = table(8 * k + min(lane, 7));
         int pb = -1;
         if (lane < 8 && 8 * k + lane < it.n_list) {
           pb = ent;
           if (pb < 0 || pb >= p.num_blocks) {
-            if (half == 0) set_error(p.err, PA_EFLAG_BAD_BLOCK_ID);
+            if (half == 0) {
+              set_error(p.err, PA_EFLAG_BAD_BLOCK_ID);
+              atomicOr(&flags[2 + (ii >> 5)], 1 << (ii & 31));
+            }
             pb = -1;
           }
         }
@@ -692,7 +737,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const bool row_ok = tq0 + tok < it.t_end;
       const int row_pos = it.first_pos + tq0 + tok;
       const int row_lo = p.window > 0 ? max(0, row_pos - p.window + 1) : 0;
-      const int kbase0 = (it.kb0 - (ANCH ? it.ab : 0)) * PA_BLOCK_SIZE;  // position of list column 0, window part
+      // position of this item's (part's) first column, window part, and the anchors from there on
+      const int kbase0 = (it.kb0 - (ANCH ? it.ab : 0)) * PA_BLOCK_SIZE + 128 * it.k0;
+      const int an0 = p.anchors - 128 * it.k0;
       float m_run = kNegInfTc, l_run = 0.f;
       const float sl = FOLD ? p.scale_log2 * folded_scale(p.k_scales[it.h_kv]) : p.scale_log2;
       for (int k = 0; ok && k < nt; ++k) {
@@ -714,7 +761,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int q = 0; q < 4; ++q) {
             const int c0 = kbase + 32 * q;
             uint32_t hide = below(row_lo - c0);
-            if constexpr (ANCH) hide &= ~below(p.anchors - 128 * k - 32 * q);  // anchors
+            if constexpr (ANCH) hide &= ~below(an0 - 128 * k - 32 * q);  // anchors
             const uint32_t keep = row_ok ? below(row_pos - c0 + 1) & ~hide : 0u;
             if (__all_sync(0xffffffffu, keep == ~0u)) continue;
             uint32_t v[32];
@@ -760,7 +807,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // key row r of V: zero it when it holds no loaded in-context data (both groups write the
         // same zeros; each must see them before its own P·V)
         const int kp_r = kbase + r;
-        const bool zero_row = (kp_r < it.kv_lo && !(ANCH && 128 * k + r < p.anchors)) || kp_r >= it.loaded_end;
+        const bool zero_row = (kp_r < it.kv_lo && !(ANCH && 128 * k + r < an0)) || kp_r >= it.loaded_end;
         const int gk = g + k, vs = gk % kVStages;
         if (__any_sync(0xffffffffu, zero_row)) {
           // the stage's copies must have landed first
@@ -825,17 +872,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_arrive(&p_full[wg]);
       }
       g += nt;
-      // a table entry of the item's keys outside the pool: its rows become zero (read while the
-      // last P·V runs)
-      bool bad = false;
-      {
-        const int32_t* trow = p.block_tables + static_cast<size_t>(it.s) * p.max_blocks;
-        for (int b = lane; b < it.n_list; b += 32) {
-          const int e = trow[it.block(b)];
-          bad |= e < 0 || e >= p.num_blocks;
-        }
-        bad = __any_sync(0xffffffffu, bad);
-      }
       // output: O / l as bf16 (zeros when a wait gave up or a block id was bad), staged in the
       // ring stage of the item's last tile that this group owns: K for query tile 0, V for 1.
       // o_done of the last tile follows every product of the CTA that reads either, so both are
@@ -845,6 +881,37 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // (coalesced).
       if (ok) ok = warp_wait(&o_done[wg], (sp - 1u) & 1u);
       tc_fence_after();
+      // (the copy warp set the bit before the copies of the item's last tile, which have been used)
+      const bool bad = (reinterpret_cast<volatile int*>(flags)[2 + (ii >> 5)] >> (ii & 31)) & 1;
+      if constexpr (ANCH) {
+        if (const int part = list[ii].part) {
+          // O as it stands, its maximum and sum, for prefill_parts_kernel (lanes hold consecutive rows, and so
+          // does a store); the ring stage that a whole item's output would pass through is released at once
+          float4* po = reinterpret_cast<float4*>(
+              reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(p.split) + part_data_off(NC)) +
+              (static_cast<size_t>((part >> 8) * (part >> 4 & 15) + (part & 15)) * 2 + wg) * kPartTile) + r;
+          const float fold = FOLD ? folded_scale(p.v_scales[it.h_kv]) : 1.f;
+#pragma unroll 1
+          for (int c = 0; ok && c < 4; ++c) {
+            uint32_t ov[32];
+            tmem_ld32(tO + 32 * c, ov);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              po[(8 * c + e / 4) * 128] = make_float4(__uint_as_float(ov[e]) * fold, __uint_as_float(ov[e + 1]) * fold,
+                                                      __uint_as_float(ov[e + 2]) * fold, __uint_as_float(ov[e + 3]) * fold);
+          }
+          // (a sum that is not a number zeroes its row, as it does in a whole item)
+          reinterpret_cast<float2*>(po - r + 32 * 128)[r] =
+              make_float2(m_run, !ok || bad || !(l_run >= 0.f) ? -1.f : l_run);
+          const int last = g - 1;
+          if (quad == 0 && lane == 0) {
+            if (wg == 0 && last + kKStages < g_tot) mbar_arrive(&k_empty[last % kKStages]);
+            if (wg == 1 && last + kVStages < g_tot) mbar_arrive(&v_empty[last % kVStages]);
+          }
+          continue;
+        }
+      }
       // zero rows are selected, not multiplied: O may hold NaN when a block was not loaded (its
       // stage keeps earlier bytes) or no key was attended
       const bool zero_out = !ok || bad || !(l_run > 0.f);
@@ -917,6 +984,62 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
+// The items that prefill_tc_kernel did in parts: per row, the parts' O weighted by 2^(m - max m) and divided by
+// the sum of their l.  CTA (item, query tile and 32 dims); a thread has a row's 16 dims.
+__global__ void __launch_bounds__(256) prefill_parts_kernel(const TcParams p, int ctas) {
+  grid_dep_wait();
+  const int2 head = p.split[0];
+  const int i = blockIdx.x, parts = head.y;
+  if (i >= head.x || parts < 2) return;
+  const uint8_t* base = reinterpret_cast<const uint8_t*>(p.split);
+  const int4 e = reinterpret_cast<const int4*>(base + part_items_off())[i];
+  const Item it = make_item<true>(p, item_rec(p, e.x, e.y, e.z));
+  const int w = blockIdx.y & 1, r = threadIdx.x & 127, c0 = (blockIdx.y >> 1) * 8 + (threadIdx.x >> 7) * 4;
+  const int tok = r / p.G, t = it.t0 + w * p.tpq + tok;
+  if (it.n_tiles == 0 || t >= it.t_end) return;
+  const int per = (it.n_tiles + parts - 1) / parts, used = (it.n_tiles + per - 1) / per;
+  const float* data = reinterpret_cast<const float*>(base + part_data_off(ctas)) +
+                      (static_cast<size_t>(i) * parts * 2 + w) * kPartTile;
+  float2 ml[8];
+  float M = kNegInfTc;
+  bool bad = false;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    ml[j] = make_float2(kNegInfTc, 0.f);
+    if (j < used) ml[j] = reinterpret_cast<const float2*>(data + static_cast<size_t>(j) * 2 * kPartTile + 128 * 128)[r];
+    bad |= ml[j].y < 0.f;
+    if (ml[j].y > 0.f) M = fmaxf(M, ml[j].x);
+  }
+  float L = 0.f, acc[16] = {};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (!(ml[j].y > 0.f)) continue;
+    const float wj = ex2(ml[j].x - M);
+    L += wj * ml[j].y;
+    const float4* o = reinterpret_cast<const float4*>(data + static_cast<size_t>(j) * 2 * kPartTile) + c0 * 128 + r;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float4 v = o[c * 128];
+      acc[4 * c] = fmaf(wj, v.x, acc[4 * c]);
+      acc[4 * c + 1] = fmaf(wj, v.y, acc[4 * c + 1]);
+      acc[4 * c + 2] = fmaf(wj, v.z, acc[4 * c + 2]);
+      acc[4 * c + 3] = fmaf(wj, v.w, acc[4 * c + 3]);
+    }
+  }
+  const bool zero = bad || !(L > 0.f);
+  const float inv = zero ? 0.f : 1.f / L;
+  uint4* out = reinterpret_cast<uint4*>(
+      p.out + (static_cast<size_t>(it.qs + t) * p.H_q + it.h_kv * p.G + (r - tok * p.G)) * 128 + c0 * 4);
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    uint32_t v[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      v[c] = zero ? 0u : pack_bf16(acc[8 * q + 2 * c] * inv, acc[8 * q + 2 * c + 1] * inv);
+    out[q] = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+}
+
 // CTAs that can run at once on the current device (persistent grid size).
 int resident_ctas() {
   static int cached[64] = {0};
@@ -941,8 +1064,7 @@ int resident_ctas() {
 pa_status launch_prefill_tc(const pa_cache_desc* desc, void* out, const void* q, const void* k_cache,
                             const void* v_cache, const int32_t* block_tables, const int32_t* q_start,
                             const int32_t* context_lens, int max_query_len, float scale, int32_t* err_flag,
-                            cudaStream_t stream, bool step, int anchors, const float* k_scales,
-                            const float* v_scales) {
+                            cudaStream_t stream, bool step, const AnchoredPrefill& a) {
   const long long slots = static_cast<long long>(desc->num_blocks) * PA_BLOCK_SIZE;
   CUtensorMap mk, mv, mq, mo;
   const int G = desc->num_q_heads / desc->num_kv_heads;
@@ -960,9 +1082,12 @@ pa_status launch_prefill_tc(const pa_cache_desc* desc, void* out, const void* q,
   p.max_blocks = desc->max_blocks_per_seq;
   p.max_q = max_query_len;
   p.window = desc->sliding_window;
-  p.anchors = anchors;
-  p.k_scales = k_scales;
-  p.v_scales = v_scales;
+  p.anchors = a.anchors;
+  p.k_scales = a.k_scales;
+  p.v_scales = a.v_scales;
+  p.split = static_cast<int2*>(a.parts);
+  p.tiles = a.tiles;
+  p.max_ctx = a.max_ctx;
   p.tpq = 128 / p.G;
   p.step = step ? 1 : 0;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
@@ -973,7 +1098,7 @@ pa_status launch_prefill_tc(const pa_cache_desc* desc, void* out, const void* q,
   p.out = static_cast<__nv_bfloat16*>(out);
   p.err = err_flag;
   auto kern = prefill_tc_kernel<false, false>;
-  if (anchors > 0 && p.window > 0) kern = k_scales ? prefill_tc_kernel<true, true> : prefill_tc_kernel<true, false>;
+  if (a.anchors > 0 && p.window > 0) kern = a.k_scales ? prefill_tc_kernel<true, true> : prefill_tc_kernel<true, false>;
   if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kern), kTcSmem)) return PA_ERR_CUDA;
   // Persistent CTAs: as many as run at once, but no more than there are work items, and enough
   // that none holds more than kMaxItems of them.
@@ -983,6 +1108,7 @@ pa_status launch_prefill_tc(const pa_cache_desc* desc, void* out, const void* q,
   long long nc = std::min<long long>(items, std::max(1, resident_ctas()));
   nc = std::max(nc, (items + kMaxItems - 1) / kMaxItems);
   nc = std::max(nc, 1LL);
+  if (p.split) nc = a.part_ctas;  // the workspace is laid out for them; there are at most kMaxItems / 2 rounds
   if (nc > 0x7FFFFFFFLL) return PA_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(nc));
@@ -994,7 +1120,15 @@ pa_status launch_prefill_tc(const pa_cache_desc* desc, void* out, const void* q,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, mk, mv, mq, mo, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kern, mk, mv, mq, mo, p) != cudaSuccess) return PA_ERR_CUDA;
+  if (!p.split) return PA_OK;
+  return launch_overlapped(prefill_parts_kernel, dim3(static_cast<unsigned>(std::min<long long>(items, nc)), 8),
+                           dim3(256), 0, stream, p, static_cast<int>(nc));
+}
+
+size_t prefill_parts_bytes(long long items, int ctas) {
+  return part_data_off(ctas) +
+         static_cast<size_t>(std::min<long long>(8 * items, 2LL * ctas)) * 2 * kPartTile * sizeof(float);
 }
 
 }  // namespace pa

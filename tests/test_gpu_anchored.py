@@ -359,6 +359,115 @@ def test_prefill_many_rows_bad_tables_and_lengths(kind):
         assert np.array_equal(out[q_start[s]:q_start[s + 1]], good[q_start[s]:q_start[s + 1]])
 
 
+# Items of many key tiles that do not fill the last round of CTAs are cut in parts and joined.
+def _parts_bytes(items):
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    return 256 + -(-sms * 16 // 256) * 256 + min(8 * items, 2 * sms) * 2 * 128 * 130 * 4
+
+
+@pytest.mark.parametrize("H_q,H_kv,chunk", [(8, 2, [300, 300]), (8, 2, [300, 1]), (2, 2, [257, 400]), (8, 8, [257, 400]),
+                                            (4, 2, [130, 300]), (16, 2, [100, 77]), (4, 1, [64, 65]), (8, 2, [0, 250])])
+@pytest.mark.parametrize("window,anchors", [(1000, 20), (1500, 3)])
+def test_prefill_parts(H_q, H_kv, chunk, window, anchors):
+    w = workload("bf16", B=2, H_q=H_q, H_kv=H_kv, ctx_list=[1533, 2301])
+    g, _, _, _ = _prefill_case(w, np.array(chunk), window, anchors)
+    items = 2 * H_kv * -(-max(chunk) // (256 * H_kv // H_q))
+    if items >= 16:  # (fewer may run on the warp-level kernel, their keys split)
+        assert N.pa_prefill_anchored_workspace_size(g.desc, max(chunk), 2301, anchors) == _parts_bytes(items)
+
+
+def test_prefill_parts_after_whole_rounds():
+    # 5 sequences' items fill one round and part of another; short sequences have items of few tiles
+    w = workload("bf16", B=5, H_q=32, H_kv=8, ctx_list=[1500, 700, 1333, 260, 1801])
+    _prefill_case(w, np.array([300, 300, 290, 260, 310]), 1000, 20)
+
+
+def test_prefill_parts_of_few_tiles():
+    # more parts than an item has tiles
+    w = workload("bf16", B=2, H_q=8, H_kv=1, ctx_list=[2000, 140])
+    _prefill_case(w, np.array([100, 140]), 1800, 20)
+
+
+@pytest.mark.parametrize("kind,sinks,H_kv", [("bf16", 4, 2), ("fp8", 0, 2), ("fp8", 4, 2), ("fp8tok", 4, 4), ("int4", 0, 4)])
+def test_prefill_parts_of_decoded_caches(kind, sinks, H_kv):
+    w = workload(kind, sinks=sinks, B=2, H_q=4 * H_kv, H_kv=H_kv, ctx_list=[1533, 1301])
+    if kind == "fp8":
+        w.k_scales[1] *= -1
+    g, _, _, _ = _prefill_case(w, np.array([300, 200]), 1000, 21)
+    assert N.pa_prefill_anchored_workspace_size(g.desc, 300, 1533, 21) == \
+        _copy_bytes(g, 300, 1533, 21, 1000) + _parts_bytes(2 * H_kv * 5)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_prefill_parts_bad_tables_and_lengths(kind):
+    w = workload(kind, B=4, H_q=8, H_kv=2, ctx_list=[1533, 1301, 1400, 1200])
+    chunk = np.array([300, 200, 128, 64])
+    g, _, q, q_start = _prefill_case(w, chunk, 1000, 20)
+    good = prefill(g, q.cuda(), q_start, w.ctx_old, 300, 20)
+    g.tables[0, 0] = w.num_blocks           # the anchors' block
+    g.tables[1, (1301 - 1) // 16] = -1      # the last block: the last query tile alone
+    g.tables_dev.copy_(torch.from_numpy(g.tables))
+    ctx = w.ctx_old.copy()
+    ctx[2] = 127  # 128 queries of a sequence of 127
+    out = prefill(g, q.cuda(), q_start, ctx, 300, 20, max_ctx=1533)
+    assert g.err_bits() == N.PA_EFLAG_BAD_BLOCK_ID | N.PA_EFLAG_CTX_OVERFLOW
+    assert np.all(out[:q_start[1]] == 0) and np.all(out[q_start[2] - 8:q_start[3]] == 0)
+    first = slice(q_start[1], q_start[1] + 128)  # other cuts than before, so other roundings
+    assert np.abs(out[first] - good[first]).max() < 2.0 ** -6 * np.abs(good[first]).max()
+    rest = slice(q_start[3], q_start[4])
+    assert np.abs(out[rest] - good[rest]).max() < 2.0 ** -6 * np.abs(good[rest]).max()
+
+
+def test_prefill_parts_context_beyond_the_declared_one():
+    w = workload("bf16", B=2, H_q=8, H_kv=2, ctx_list=[1533, 1301])
+    g, _ = states(w, 1000)
+    q = torch.randn(400, w.H_q, w.D, generator=torch.Generator().manual_seed(9)).to(torch.bfloat16).cuda()
+    out = prefill(g, q, np.array([0, 200, 400]), w.ctx_old, 200, 20, max_ctx=1532)
+    assert N.pa_prefill_anchored_workspace_size(g.desc, 200, 1532, 20) == _parts_bytes(2 * 2 * 4)
+    assert g.err_bits() == N.PA_EFLAG_CTX_OVERFLOW
+    assert np.all(out[:200] == 0) and np.all(np.abs(out[200:]).max(axis=(1, 2)) > 0)
+
+
+def test_prefill_parts_replayed_with_other_lengths():
+    w = workload("bf16", B=2, H_q=8, H_kv=2, ctx_list=[1533, 1301])
+    g, o = states(w, 1000)
+    q_start = np.array([0, 200, 330])
+    q = torch.randn(330, w.H_q, w.D, generator=torch.Generator().manual_seed(9)).to(torch.bfloat16)
+    out = torch.zeros(330, w.H_q, w.D, dtype=torch.bfloat16, device="cuda")
+    n = N.pa_prefill_anchored_workspace_size(g.desc, 200, 1533, 20)
+    ws, ctx, qd, qs = torch.empty(n, dtype=torch.uint8, device="cuda"), gpu(w.ctx_old), q.cuda(), gpu(q_start)
+
+    def call():
+        N.pa_prefill_attention_anchored(g.desc, out, qd, g.k, g.v, g.tables_dev, qs, ctx, 200, 1533, w.scale, 20, ws, n,
+                                        g.err)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            call()
+            call()
+    torch.cuda.synchronize()
+    qv = O.bf16_bits_to_f64(bf16_bits(q))
+    for lens, starts in (([1533, 1301], [0, 200, 330]), ([200, 1290], [0, 200, 201]), ([1500, 1301], [0, 0, 130])):
+        ctx.copy_(gpu(lens))
+        qs.copy_(gpu(np.array(starts)))
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        for s, c in enumerate(lens):
+            rows = slice(starts[s], starts[s + 1])
+            if starts[s] == starts[s + 1]:
+                continue
+            mask = O.anchored_mask(c, starts[s + 1] - starts[s], 1000, 20)
+            K, V = O.gather_positions(o.cache, s, o.tables[s], np.arange(c))
+            ref, mag = O.masked_attention(qv[rows], K, V, w.scale, mask)
+            assert_within(to_f64(out)[rows], ref, tolerance(ref, mag), f"replay at {lens}, sequence {s}")
+    assert g.err_bits() == 0
+
+
 def test_prefill_few_rows_over_a_long_window():
     # up to 32 shares of the keys, one of them empty, and sequences without keys in some
     for chunk, G in (([1, 3], 1), ([8, 2], 4), ([5, 7], 7)):
