@@ -420,11 +420,12 @@ pa_status pa_prefill_step_ws(const pa_cache_desc* desc, void* out, const void* q
  *                     attend, so its size goes with W + max_query_len + num_anchor, not with the
  *                     context.  Where the query tiles do not fill the GPU, the keys of a tile are
  *                     split over several CTAs, and it takes their partial rows: which tiles are split
- *                     depends on the whole batch, and so do a sequence's last bits.  The size is 0 when the call needs none
- *                     (workspace may then be NULL) or an argument is invalid; ask for it on the
- *                     device that the call runs on.  With anchors and a window, 8-bit caches with
- *                     per-head scales keep their bare codes there (the scales multiply the scores and
- *                     the output), so that K and V are not rounded; other decoded values are, to bf16.
+ *                     depends on the whole batch, and so do a sequence's last bits.  The size is 0
+ *                     when the call needs none (workspace may then be NULL) or an argument is
+ *                     invalid; ask for it on the device that the call runs on.
+ * With anchors and a window, an 8-bit cache's per-head scales (positive ones) multiply the scores and the
+ * output, so that its K and V are not rounded; other decoded values, and sink rows divided by such a scale,
+ * are rounded to bf16.
  * A sequence that breaks pa_prefill_attention's rules, or (with a workspace) has a context beyond
  * max_context_len, sets PA_EFLAG_CTX_OVERFLOW and gets zero rows; other rules, device errors and
  * host errors as pa_prefill_attention_ws. */

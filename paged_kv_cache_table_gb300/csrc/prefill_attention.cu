@@ -65,6 +65,9 @@ struct PrefillParams {
   const __nv_bfloat16* k_sink;
   const __nv_bfloat16* v_sink;
   size_t extra_offset;
+  // pa_prefill_attention_anchored, 8-bit caches with per-head scales: K and V stay bare codes (sink rows are
+  // divided by the scale), and the scores and the output take the scales (folded_scale of each).
+  int fold;
   // Split keys (pa_prefill_attention_anchored with few query tiles): `splits` CTAs share a tile's blocks
   // and leave partial rows part[((s * max_q + token) * H_q + h) * splits + split][D + 4] = (o, m, l), l = -1
   // after a bad block id, which prefill_join_kernel combines.  1: none.
@@ -128,11 +131,14 @@ struct PrefillRows {
   uint32_t qa[KT][4];  // Q fragments (A operand, rows x head_dim)
   float o[NT][4];
   float m[2], l[2];
+  float k_scale, v_scale;  // of the scores (log2 units), of the output
   bool bad;
 
   __device__ __forceinline__ void init(const PrefillParams& p, int warp, int lane_, int qs, int h_kv, int t0,
                                        int t_end, int first_pos) {
     lane = lane_;
+    k_scale = p.fold ? p.scale_log2 * folded_scale(p.k_scales[h_kv]) : p.scale_log2;
+    v_scale = p.fold ? folded_scale(p.v_scales[h_kv]) : 1.f;
     t4 = lane >> 2;
     tq = lane & 3;
     wt0 = t0 + warp * p.tpw;  // this warp's first query token (chunk index)
@@ -199,7 +205,7 @@ struct PrefillRows {
           const int kp = kbase_pos + nt * 8 + 2 * tq + jj;
           const bool ok = row_ok[half] && kp <= row_pos[half] &&
                           (p.window <= 0 || kp > row_pos[half] - p.window || kp < p.anchors);
-          const float v = ok ? sacc[nt][2 * half + jj] * p.scale_log2 : kNegInfP;
+          const float v = ok ? sacc[nt][2 * half + jj] * k_scale : kNegInfP;
           sv[half][nt][jj] = v;
           bm[half] = fmaxf(bm[half], v);
         }
@@ -285,7 +291,7 @@ struct PrefillRows {
                                   p.splits * (D + 4) + static_cast<size_t>(split) * (D + 4);
 #pragma unroll
         for (int i = 0; i < NT; ++i)
-          *reinterpret_cast<float2*>(row + i * 8 + 2 * tq) = make_float2(o[i][2 * half], o[i][2 * half + 1]);
+          *reinterpret_cast<float2*>(row + i * 8 + 2 * tq) = make_float2(o[i][2 * half] * v_scale, o[i][2 * half + 1] * v_scale);
         if (tq == 0) *reinterpret_cast<float2*>(row + D) = make_float2(m[half], bad ? -1.f : l[half]);
       }
       return;
@@ -294,7 +300,7 @@ struct PrefillRows {
     for (int half = 0; half < 2; ++half) {
       if (!row_ok[half]) continue;
       const int r = t4 + 8 * half;
-      const float inv = (bad || !(l[half] > 0.f)) ? 0.f : 1.f / l[half];
+      const float inv = (bad || !(l[half] > 0.f)) ? 0.f : v_scale / l[half];
       __nv_bfloat16* orow = p.out + (static_cast<size_t>(qs + wt0 + r / p.G) * p.H_q + h_kv * p.G + r % p.G) * D;
 #pragma unroll
       for (int i = 0; i < NT; ++i)
@@ -512,11 +518,24 @@ struct DqPiece {
     }
   }
 
+  // The same for a cache whose per-head scales are applied later: bare codes, and sink rows divided by the scale.
+  __device__ __forceinline__ void decode_folded(const PrefillParams& p, int t, int h, uint32_t (&out)[16]) {
+    const float whole = (t ? p.v_scales : p.k_scales)[h], f = folded_scale(whole);
+    if (!sink && f == whole) sc = 1.f;
+    decode(t, out);
+    if (!sink) return;
+    const float inv = __frcp_rn(f);
+#pragma unroll
+    for (int u = 0; u < 16; ++u)
+      out[u] = pack_bf16(__uint_as_float(out[u] << 16) * inv, __uint_as_float(out[u] & 0xFFFF0000u) * inv);
+  }
+
   // Write the piece's 32 values as bf16 into row `row` of a [16 rows][128 B]-per-chunk tile with
   // the 128-byte swizzle: dims 32g + 8u .. + 7 form 16-byte unit 4g + u of the row.
-  __device__ __forceinline__ void store(int t, uint8_t* tile, int row, int g) const {
+  __device__ __forceinline__ void store(const PrefillParams& p, int t, int h, uint8_t* tile, int row, int g) {
     uint32_t out[16];
-    decode(t, out);
+    if (KIND == 1 && p.fold) decode_folded(p, t, h, out);
+    else decode(t, out);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int du = 4 * g + u, c = du >> 3, uu = du & 7;
@@ -584,7 +603,7 @@ __global__ void __launch_bounds__(kPfWarps * 32)
   if (n_blocks > 0) load(0, e);
   for (int k = 0; k < n_blocks; ++k) {
     uint8_t* wk = work[k & 1];
-    if (piece && e != -2) cur.store(pt, wk + pt * TILE, pr, pg);
+    if (piece && e != -2) cur.store(p, pt, h_kv, wk + pt * TILE, pr, pg);
     if (tid == 0) {
       bad_blk[k & 1] = e == -2 ? 1 : 0;
       if (e == -2) set_error(p.err, PA_EFLAG_BAD_BLOCK_ID);
@@ -658,7 +677,7 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillParams p
 // the chunk's queries can attend: CTA (i, s) takes the i-th of them, the anchors' blocks and then the
 // window's, into block s * cap + i, and dense[s][b] of that logical block b names it; the entries of
 // other blocks are not written (nor read).
-// fold (8-bit caches with per-head scales): the pool holds the bare codes, which bf16 represents exactly,
+// p.fold (8-bit caches with per-head scales): the pool holds the bare codes, which bf16 represents exactly,
 // and sink rows divided by the scale; the attention kernel multiplies the scores by k_scales and the
 // output by v_scales.  Decoded values (code times scale) would each be rounded to bf16: 3.9e-3 against
 // 2.4e-3 of the output's norm on four chunks of 1024 over a window of 2048.
@@ -666,7 +685,7 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillParams p
 template <int D, int KIND>
 __global__ void __launch_bounds__(256)
     prefill_expand_kernel(const PrefillParams p, int mb, __nv_bfloat16* kx, __nv_bfloat16* vx, int32_t* dense,
-                          int cap, bool fold) {
+                          int cap) {
   constexpr int GROUPS = D / 32;
   const int s = blockIdx.y;
   int b = blockIdx.x;
@@ -703,19 +722,8 @@ __global__ void __launch_bounds__(256)
     DqPiece<D, KIND> pc;
     pc.load(p, t, s, h, b * PA_BLOCK_SIZE + r, static_cast<size_t>(e) * PA_BLOCK_SIZE + r, g);
     uint32_t out[16];
-    if (KIND == 1 && fold) {
-      const float whole = (t ? p.v_scales : p.k_scales)[h], f = folded_scale(whole);
-      if (!pc.sink && f == whole) pc.sc = 1.f;
-      pc.decode(t, out);
-      if (pc.sink) {
-        const float inv = __frcp_rn(f);
-#pragma unroll
-        for (int u = 0; u < 16; ++u)
-          out[u] = pack_bf16(__uint_as_float(out[u] << 16) * inv, __uint_as_float(out[u] & 0xFFFF0000u) * inv);
-      }
-    } else {
-      pc.decode(t, out);
-    }
+    if (KIND == 1 && p.fold) pc.decode_folded(p, t, h, out);
+    else pc.decode(t, out);
     uint4* dst = reinterpret_cast<uint4*>((t ? vx : kx) + ((xb * PA_BLOCK_SIZE + r) * p.H_kv + h) * D + 32 * g);
 #pragma unroll
     for (int u = 0; u < 4; ++u) dst[u] = make_uint4(out[4 * u], out[4 * u + 1], out[4 * u + 2], out[4 * u + 3]);
@@ -780,6 +788,7 @@ PrefillParams prefill_params(const pa_cache_desc* desc, void* out, const void* q
   p.v_scales = desc->v_scales;
   p.k_sink = static_cast<const __nv_bfloat16*>(desc->k_sink);
   p.v_sink = static_cast<const __nv_bfloat16*>(desc->v_sink);
+  p.fold = 0;
   p.splits = 1;
   p.max_ctx = 0x7FFFFFFF;
   p.part = nullptr;
@@ -858,6 +867,11 @@ size_t prefill_ws_bytes(const pa_cache_desc* d, int max_ctx, int* mb_out) {
   const size_t pool = static_cast<size_t>(d->num_seqs) * mb * PA_BLOCK_SIZE * d->num_kv_heads * 128 * 2;
   return table + 2 * pool;
 #endif
+}
+
+// Whether pa_prefill_attention_anchored applies a cache's per-head scales to the scores and the output.
+bool prefill_folds(const pa_cache_desc* d, int anchors) {
+  return anchors > 0 && d->sliding_window > 0 && d->k_dtype == PA_FP8_E4M3;
 }
 
 // How pa_prefill_attention_anchored runs: the tensor-core kernel, over a decoded copy of *cap blocks per
@@ -974,25 +988,24 @@ pa_status prefill_expanded(const pa_cache_desc* desc, void* out, const void* q, 
                            const void* v_cache, const int32_t* block_tables, const int32_t* q_start,
                            const int32_t* context_lens, int max_query_len, float scale, int mb, void* workspace,
                            int32_t* err_flag, void* stream, int cap = 0, AnchoredPrefill a = {}) {
-  const PrefillParams p = prefill_params(desc, out, q, k_cache, v_cache, block_tables, q_start, context_lens,
-                                         max_query_len, scale, err_flag, a.anchors);
+  PrefillParams p = prefill_params(desc, out, q, k_cache, v_cache, block_tables, q_start, context_lens,
+                                   max_query_len, scale, err_flag, a.anchors);
+  p.fold = prefill_folds(desc, a.anchors) ? 1 : 0;
   const int per_seq = cap > 0 ? cap : mb;
   const size_t table = (static_cast<size_t>(desc->num_seqs) * mb * 4 + 255) / 256 * 256;
   const size_t pool = static_cast<size_t>(desc->num_seqs) * per_seq * PA_BLOCK_SIZE * desc->num_kv_heads * 128 * 2;
   int32_t* dense = static_cast<int32_t*>(workspace);
   auto* kx = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(workspace) + table);
   auto* vx = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(workspace) + table + pool);
-  // per-head scales are applied by the attention kernel of the anchored call
-  const bool fold = cap > 0 && a.anchors > 0 && desc->sliding_window > 0 && desc->k_dtype == PA_FP8_E4M3;
   cudaStream_t s = as_stream(stream);
   const dim3 grid(per_seq, desc->num_seqs), block(256);
   pa_status st;
-  if (is_int4(desc)) st = launch_overlapped(prefill_expand_kernel<128, 2>, grid, block, 0, s, p, mb, kx, vx, dense, cap, fold);
+  if (is_int4(desc)) st = launch_overlapped(prefill_expand_kernel<128, 2>, grid, block, 0, s, p, mb, kx, vx, dense, cap);
   else if (has_token_scales(desc))
-    st = launch_overlapped(prefill_expand_kernel<128, 3>, grid, block, 0, s, p, mb, kx, vx, dense, cap, fold);
+    st = launch_overlapped(prefill_expand_kernel<128, 3>, grid, block, 0, s, p, mb, kx, vx, dense, cap);
   else if (is_quantized(desc))
-    st = launch_overlapped(prefill_expand_kernel<128, 1>, grid, block, 0, s, p, mb, kx, vx, dense, cap, fold);
-  else st = launch_overlapped(prefill_expand_kernel<128, 0>, grid, block, 0, s, p, mb, kx, vx, dense, cap, fold);
+    st = launch_overlapped(prefill_expand_kernel<128, 1>, grid, block, 0, s, p, mb, kx, vx, dense, cap);
+  else st = launch_overlapped(prefill_expand_kernel<128, 0>, grid, block, 0, s, p, mb, kx, vx, dense, cap);
   if (st != PA_OK) return st;
   pa_cache_desc x = *desc;  // the bf16 pool: every attended block, sinks included, in place
   x.k_dtype = x.v_dtype = PA_BF16;
@@ -1001,7 +1014,7 @@ pa_status prefill_expanded(const pa_cache_desc* desc, void* out, const void* q, 
   x.num_sink = 0;
   x.num_blocks = desc->num_seqs * per_seq;
   x.max_blocks_per_seq = mb;
-  if (fold) {
+  if (p.fold) {
     a.k_scales = desc->k_scales;
     a.v_scales = desc->v_scales;
   }
@@ -1075,6 +1088,7 @@ extern "C" pa_status pa_prefill_attention_anchored(const pa_cache_desc* desc, vo
   if (pl.warps) {
     pa::PrefillParams p = pa::prefill_params(desc, out, q, k_cache, v_cache, block_tables, q_start, context_lens,
                                              max_query_len, scale, err_flag, anchors);
+    p.fold = pa::prefill_folds(desc, anchors) ? 1 : 0;
     p.splits = pl.splits;
     if (pl.splits > 1) {
       p.max_ctx = max_context_len;
