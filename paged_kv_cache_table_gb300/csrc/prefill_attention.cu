@@ -76,28 +76,32 @@ struct PrefillParams {
   float* part;
 };
 
+// ANCH here and below: a call with anchors; without it nothing of anchors, folded scales and split keys is in
+// the code (kept at run time it cost the calls without them up to 10 %, over sinks at head_dim 64 26 %).
+template <bool ANCH>
 __device__ __forceinline__ bool prefill_valid(const PrefillParams& p, int n, int ctx) {
-  return n >= 0 && n <= ctx && n <= p.max_q && ctx <= p.max_blocks * PA_BLOCK_SIZE && ctx <= p.max_ctx;
+  return n >= 0 && n <= ctx && n <= p.max_q && ctx <= p.max_blocks * PA_BLOCK_SIZE && (!ANCH || ctx <= p.max_ctx);
 }
 
 // The blocks a query tile reads: [0, ab), then [kb0, kb0 + n - ab); ab = 0 without anchors, and
 // when the anchors' blocks reach kb0 (the list is then one run from block 0).  kv_lo: first key of
 // the window part (0 when the anchors reach it); kv_end: one past the last key.
+template <bool ANCH>
 struct BlockList {
   int ab, kb0, n, lo, k0 = 0;
   __device__ __forceinline__ BlockList(const PrefillParams& p, int kv_lo, int kv_end) : lo(kv_lo) {
     kb0 = kv_lo / PA_BLOCK_SIZE;
-    ab = p.window > 0 ? (p.anchors + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE : 0;
-    if (ab >= kb0) {
+    ab = ANCH && p.window > 0 ? (p.anchors + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE : 0;
+    if (ANCH && ab >= kb0) {
       if (ab > 0) kb0 = 0;
       ab = 0;
     }
     n = ab + (kv_end + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE - kb0;
   }
-  __device__ __forceinline__ int block(int k) const { return k + k0 < ab ? k + k0 : kb0 + k + k0 - ab; }
+  __device__ __forceinline__ int block(int k) const { return !ANCH ? kb0 + k : k + k0 < ab ? k + k0 : kb0 + k + k0 - ab; }
   // The share `split` of `splits` of the list.
   __device__ __forceinline__ void cut(int split, int splits) {
-    if (splits == 1) return;
+    if (!ANCH || splits == 1) return;
     const int per = (n + splits - 1) / splits;
     k0 = min(n, split * per);
     n = min(per, n - k0);
@@ -106,14 +110,15 @@ struct BlockList {
   // another block is not looked at (it may have been released).
   __device__ __forceinline__ bool paged(const PrefillParams& p, int b) const {
     const int first = max(p.num_sink, b * PA_BLOCK_SIZE), end = (b + 1) * PA_BLOCK_SIZE;
-    return end > max(first, lo) || min(p.anchors, end) > first;
+    return ANCH ? end > max(first, lo) || min(p.anchors, end) > first : !(b * PA_BLOCK_SIZE + PA_BLOCK_SIZE <= p.num_sink);
   }
 };
 
 // First key of the window of the query at position pos; 0 when the anchors reach it.
+template <bool ANCH>
 __device__ __forceinline__ int key_lo(const PrefillParams& p, int pos) {
   const int lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-  return lo <= p.anchors ? 0 : lo;
+  return ANCH && lo <= p.anchors ? 0 : lo;
 }
 
 // One consumer warp's 16 query rows of a prefill tile: row r = (token r / G, query head r % G) of
@@ -121,7 +126,7 @@ __device__ __forceinline__ int key_lo(const PrefillParams& p, int pos) {
 // with the queries as M; P is reused straight from the S accumulator registers as the A operand
 // of P·V.  block() takes one 16-key block whose K and V sit in shared memory as bf16 tiles of
 // [16 slots][128 bytes] per 128-byte chunk of the head row, with the 128-byte swizzle.
-template <int D>
+template <int D, bool ANCH>
 struct PrefillRows {
   static constexpr int KT = D / 16;  // k-steps of Q·Kᵀ
   static constexpr int NT = D / 8;   // n-tiles of P·V
@@ -137,15 +142,15 @@ struct PrefillRows {
   __device__ __forceinline__ void init(const PrefillParams& p, int warp, int lane_, int qs, int h_kv, int t0,
                                        int t_end, int first_pos) {
     lane = lane_;
-    k_scale = p.fold ? p.scale_log2 * folded_scale(p.k_scales[h_kv]) : p.scale_log2;
-    v_scale = p.fold ? folded_scale(p.v_scales[h_kv]) : 1.f;
+    k_scale = ANCH && p.fold ? p.scale_log2 * folded_scale(p.k_scales[h_kv]) : p.scale_log2;
+    v_scale = ANCH && p.fold ? folded_scale(p.v_scales[h_kv]) : 1.f;
     t4 = lane >> 2;
     tq = lane & 3;
     wt0 = t0 + warp * p.tpw;  // this warp's first query token (chunk index)
     w_tokens = max(0, min(p.tpw, t_end - wt0));
     w_last_pos = first_pos + wt0 + w_tokens - 1;  // last query position of this warp
     // lowest key any row of this warp reads (its first token's window start)
-    w_lo = key_lo(p, first_pos + wt0);
+    w_lo = key_lo<ANCH>(p, first_pos + wt0);
     // rows past the tokens are padding
     const int rows_used = w_tokens * p.G;
 #pragma unroll
@@ -176,7 +181,7 @@ struct PrefillRows {
   // One block of 16 keys at positions kbase_pos.. (kv_end: first key past the tile's queries).
   __device__ __forceinline__ void block(const PrefillParams& p, const uint8_t* kt, const uint8_t* vt, int kbase_pos,
                                         int kv_end) {
-    if (!(w_tokens > 0 && kbase_pos <= w_last_pos && (kbase_pos + PA_BLOCK_SIZE > w_lo || kbase_pos < p.anchors)))
+    if (!(w_tokens > 0 && kbase_pos <= w_last_pos && (kbase_pos + PA_BLOCK_SIZE > w_lo || (ANCH && kbase_pos < p.anchors))))
       return;
     // S = Q Kᵀ for the 16 keys (two n-tiles of 8)
     float sacc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -204,8 +209,8 @@ struct PrefillRows {
         for (int jj = 0; jj < 2; ++jj) {
           const int kp = kbase_pos + nt * 8 + 2 * tq + jj;
           const bool ok = row_ok[half] && kp <= row_pos[half] &&
-                          (p.window <= 0 || kp > row_pos[half] - p.window || kp < p.anchors);
-          const float v = ok ? sacc[nt][2 * half + jj] * k_scale : kNegInfP;
+                          (p.window <= 0 || kp > row_pos[half] - p.window || (ANCH && kp < p.anchors));
+          const float v = ok ? sacc[nt][2 * half + jj] * (ANCH ? k_scale : p.scale_log2) : kNegInfP;
           sv[half][nt][jj] = v;
           bm[half] = fmaxf(bm[half], v);
         }
@@ -256,7 +261,7 @@ struct PrefillRows {
     uint32_t vlo = 0xFFFFFFFFu, vhi = 0xFFFFFFFFu;
     if (kbase_pos + PA_BLOCK_SIZE > kv_end || kbase_pos < w_lo) {
       const int hi = kv_end - kbase_pos, lo = w_lo - kbase_pos, an = p.anchors - kbase_pos;
-      auto keep = [&](int r) { return r < hi && (r >= lo || r < an); };
+      auto keep = [&](int r) { return r < hi && (r >= lo || (ANCH && r < an)); };
       vlo = (keep(2 * tq) ? 0x0000FFFFu : 0u) | (keep(2 * tq + 1) ? 0xFFFF0000u : 0u);
       vhi = (keep(2 * tq + 8) ? 0x0000FFFFu : 0u) | (keep(2 * tq + 9) ? 0xFFFF0000u : 0u);
     }
@@ -282,7 +287,7 @@ struct PrefillRows {
       l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
       l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
     }
-    if (p.splits > 1) {
+    if (ANCH && p.splits > 1) {
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         if (!row_ok[half]) continue;
@@ -300,7 +305,7 @@ struct PrefillRows {
     for (int half = 0; half < 2; ++half) {
       if (!row_ok[half]) continue;
       const int r = t4 + 8 * half;
-      const float inv = (bad || !(l[half] > 0.f)) ? 0.f : v_scale / l[half];
+      const float inv = (bad || !(l[half] > 0.f)) ? 0.f : (ANCH ? v_scale : 1.f) / l[half];
       __nv_bfloat16* orow = p.out + (static_cast<size_t>(qs + wt0 + r / p.G) * p.H_q + h_kv * p.G + r % p.G) * D;
 #pragma unroll
       for (int i = 0; i < NT; ++i)
@@ -310,7 +315,7 @@ struct PrefillRows {
   }
 };
 
-template <int D>
+template <int D, bool ANCH>
 __global__ void __launch_bounds__(kPfThreads)
     prefill_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    const PrefillParams p) {
@@ -321,14 +326,14 @@ __global__ void __launch_bounds__(kPfThreads)
   __shared__ int bad_stage[kPfStages];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int s = blockIdx.y, h_kv = blockIdx.z / p.splits, split = blockIdx.z % p.splits, tile = blockIdx.x;
+  const int s = blockIdx.y, h_kv = ANCH ? blockIdx.z / p.splits : blockIdx.z, split = ANCH ? blockIdx.z % p.splits : 0, tile = blockIdx.x;
   // launched with programmatic dependent launch: the previous kernel of the stream may still be
   // writing any input (q, lengths, tables, cache), so everything below waits for it
   grid_dep_wait();
   const int qs = p.q_start[s];
   const int n = p.q_start[s + 1] - qs;
   const int ctx = p.context_lens[s];
-  if (!prefill_valid(p, n, ctx)) {
+  if (!prefill_valid<ANCH>(p, n, ctx)) {
     if (tile == 0 && h_kv == 0 && tid == 0) set_error(p.err, PA_EFLAG_CTX_OVERFLOW);
     // zero the rows this CTA would have produced (those inside the query range it can see)
     const int rows = min(max(n, 0), p.max_q);
@@ -342,7 +347,7 @@ __global__ void __launch_bounds__(kPfThreads)
   const int first_pos = ctx - n;
   const int t_end = min(n, t0 + p.q_tile);
   const int kv_end = first_pos + t_end;  // keys [kv_lo, kv_end) are visible to this tile
-  BlockList bl(p, key_lo(p, first_pos + t0), kv_end);  // the logical blocks read
+  BlockList<ANCH> bl(p, key_lo<ANCH>(p, first_pos + t0), kv_end);  // the logical blocks read
   bl.cut(split, p.splits);
   const int n_blocks = bl.n;
 
@@ -401,7 +406,7 @@ __global__ void __launch_bounds__(kPfThreads)
   }
 
   // ------------------------------ consumers ------------------------------
-  PrefillRows<D> w;
+  PrefillRows<D, ANCH> w;
   w.init(p, warp, lane, qs, h_kv, t0, t_end, first_pos);
   for (int k = 0; k < n_blocks; ++k) {
     const int st = k % kPfStages;
@@ -532,9 +537,10 @@ struct DqPiece {
 
   // Write the piece's 32 values as bf16 into row `row` of a [16 rows][128 B]-per-chunk tile with
   // the 128-byte swizzle: dims 32g + 8u .. + 7 form 16-byte unit 4g + u of the row.
+  template <bool ANCH>
   __device__ __forceinline__ void store(const PrefillParams& p, int t, int h, uint8_t* tile, int row, int g) {
     uint32_t out[16];
-    if (KIND == 1 && p.fold) decode_folded(p, t, h, out);
+    if (ANCH && KIND == 1 && p.fold) decode_folded(p, t, h, out);
     else decode(t, out);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -545,7 +551,7 @@ struct DqPiece {
   }
 };
 
-template <int D, int KIND>
+template <int D, int KIND, bool ANCH>
 __global__ void __launch_bounds__(kPfWarps * 32)
     prefill_dq_kernel(const PrefillParams p) {
   constexpr int NC = D * 2 / 128;          // 128-byte chunks per bf16 head row
@@ -556,12 +562,12 @@ __global__ void __launch_bounds__(kPfWarps * 32)
   __shared__ int bad_blk[2];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int s = blockIdx.y, h_kv = blockIdx.z / p.splits, split = blockIdx.z % p.splits, tile = blockIdx.x;
+  const int s = blockIdx.y, h_kv = ANCH ? blockIdx.z / p.splits : blockIdx.z, split = ANCH ? blockIdx.z % p.splits : 0, tile = blockIdx.x;
   grid_dep_wait();  // the previous kernel of the stream may still be writing any input
   const int qs = p.q_start[s];
   const int n = p.q_start[s + 1] - qs;
   const int ctx = p.context_lens[s];
-  if (!prefill_valid(p, n, ctx)) {
+  if (!prefill_valid<ANCH>(p, n, ctx)) {
     if (tile == 0 && h_kv == 0 && tid == 0) set_error(p.err, PA_EFLAG_CTX_OVERFLOW);
     const int rows = min(max(n, 0), p.max_q);
     for (int t = tile * p.q_tile + warp; t < min(rows, (tile + 1) * p.q_tile); t += kPfWarps)
@@ -574,12 +580,12 @@ __global__ void __launch_bounds__(kPfWarps * 32)
   const int first_pos = ctx - n;
   const int t_end = min(n, t0 + p.q_tile);
   const int kv_end = first_pos + t_end;
-  BlockList bl(p, key_lo(p, first_pos + t0), kv_end);
+  BlockList<ANCH> bl(p, key_lo<ANCH>(p, first_pos + t0), kv_end);
   bl.cut(split, p.splits);
   const int n_blocks = bl.n;
-  const int32_t* trow = p.block_tables + static_cast<size_t>(s) * p.max_blocks;
+  const int32_t* trow = p.block_tables + static_cast<size_t>(s) * p.max_blocks + (ANCH ? 0 : bl.kb0);
 
-  PrefillRows<D> w;
+  PrefillRows<D, ANCH> w;
   w.init(p, warp, lane, qs, h_kv, t0, t_end, first_pos);
 
   // this thread's piece: tensor pt, token row pr, 32-dim group pg
@@ -591,7 +597,7 @@ __global__ void __launch_bounds__(kPfWarps * 32)
   auto entry = [&](int k) -> int {
     const int kb = bl.block(k);
     if (!bl.paged(p, kb)) return -1;
-    const int e = trow[kb];
+    const int e = trow[ANCH ? kb : k];
     return (e < 0 || e >= p.num_blocks) ? -2 : e;
   };
   auto load = [&](int k, int e) {
@@ -603,7 +609,7 @@ __global__ void __launch_bounds__(kPfWarps * 32)
   if (n_blocks > 0) load(0, e);
   for (int k = 0; k < n_blocks; ++k) {
     uint8_t* wk = work[k & 1];
-    if (piece && e != -2) cur.store(p, pt, h_kv, wk + pt * TILE, pr, pg);
+    if (piece && e != -2) cur.template store<ANCH>(p, pt, h_kv, wk + pt * TILE, pr, pg);
     if (tid == 0) {
       bad_blk[k & 1] = e == -2 ? 1 : 0;
       if (e == -2) set_error(p.err, PA_EFLAG_BAD_BLOCK_ID);
@@ -632,7 +638,7 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillParams p
   const long long s = row / p.H_q / p.max_q;
   if (s >= p.B) return;
   const int qs = p.q_start[s], n = p.q_start[s + 1] - qs;
-  if (!prefill_valid(p, n, p.context_lens[s]) || tok >= n) return;
+  if (!prefill_valid<true>(p, n, p.context_lens[s]) || tok >= n) return;
   const float* part = p.part + static_cast<size_t>(row) * p.splits * (D + 4);
   float2 ml = make_float2(kNegInfP, 0.f);
   if (lane < p.splits) ml = *reinterpret_cast<const float2*>(part + static_cast<size_t>(lane) * (D + 4) + D);
@@ -695,9 +701,9 @@ __global__ void __launch_bounds__(256)
   const bool valid = n >= 0 && n <= ctx && n <= p.max_q && ctx <= p.max_blocks * PA_BLOCK_SIZE &&
                      ctx <= mb * PA_BLOCK_SIZE;
   // the positions the chunk's queries attend: from the first query's window start to ctx - 1
-  const int lo = key_lo(p, ctx - n);
+  const int lo = key_lo<true>(p, ctx - n);
   int first = lo / PA_BLOCK_SIZE;  // first block to decode
-  const BlockList bl(p, lo, ctx);
+  const BlockList<true> bl(p, lo, ctx);
   if (cap > 0) {
     b = bl.block(b);
     first = 0;
@@ -796,6 +802,22 @@ PrefillParams prefill_params(const pa_cache_desc* desc, void* out, const void* q
   return p;
 }
 
+template <bool ANCH>
+pa_status launch_warps(const pa_cache_desc* desc, const PrefillParams& p, bool dq, dim3 grid, const CUtensorMap& mk,
+                       const CUtensorMap& mv, cudaStream_t s) {
+  if (dq) {  // 8-bit and INT4 caches have head_dim 128 (validate_desc)
+    const dim3 block(kPfWarps * 32);
+    if (is_int4(desc)) return launch_overlapped(prefill_dq_kernel<128, 2, ANCH>, grid, block, 0, s, p);
+    if (has_token_scales(desc)) return launch_overlapped(prefill_dq_kernel<128, 3, ANCH>, grid, block, 0, s, p);
+    if (is_quantized(desc)) return launch_overlapped(prefill_dq_kernel<128, 1, ANCH>, grid, block, 0, s, p);
+    if (desc->head_dim == 128) return launch_overlapped(prefill_dq_kernel<128, 0, ANCH>, grid, block, 0, s, p);
+    return launch_overlapped(prefill_dq_kernel<64, 0, ANCH>, grid, block, 0, s, p);
+  }
+  if (desc->head_dim == 128) return launch_overlapped(prefill_kernel<128, ANCH>, grid, dim3(kPfThreads), 0, s, mk, mv, p);
+  return launch_overlapped(prefill_kernel<64, ANCH>, grid, dim3(kPfThreads), 0, s, mk, mv, p);
+}
+
+
 // The warp-MMA kernels (bf16 caches without sinks by TMA, every other one decoded block by block), with
 // the keys of a tile split over p.splits CTAs.
 pa_status prefill_warps(const pa_cache_desc* desc, const PrefillParams& p, const void* k_cache, const void* v_cache,
@@ -809,19 +831,8 @@ pa_status prefill_warps(const pa_cache_desc* desc, const PrefillParams& p, const
     return PA_ERR_CUDA;
   const dim3 grid((p.max_q + p.q_tile - 1) / p.q_tile, p.B, p.H_kv * p.splits);
   cudaStream_t s = as_stream(stream);
-  pa_status st;
-  if (dq) {  // 8-bit and INT4 caches have head_dim 128 (validate_desc)
-    const dim3 block(kPfWarps * 32);
-    if (is_int4(desc)) st = launch_overlapped(prefill_dq_kernel<128, 2>, grid, block, 0, s, p);
-    else if (has_token_scales(desc)) st = launch_overlapped(prefill_dq_kernel<128, 3>, grid, block, 0, s, p);
-    else if (is_quantized(desc)) st = launch_overlapped(prefill_dq_kernel<128, 1>, grid, block, 0, s, p);
-    else if (D == 128) st = launch_overlapped(prefill_dq_kernel<128, 0>, grid, block, 0, s, p);
-    else st = launch_overlapped(prefill_dq_kernel<64, 0>, grid, block, 0, s, p);
-  } else if (D == 128) {
-    st = launch_overlapped(prefill_kernel<128>, grid, dim3(kPfThreads), 0, s, mk, mv, p);
-  } else {
-    st = launch_overlapped(prefill_kernel<64>, grid, dim3(kPfThreads), 0, s, mk, mv, p);
-  }
+  const pa_status st = p.anchors > 0 ? launch_warps<true>(desc, p, dq, grid, mk, mv, s)
+                                     : launch_warps<false>(desc, p, dq, grid, mk, mv, s);
   if (st != PA_OK || p.splits == 1) return st;
   const long long rows = static_cast<long long>(p.B) * p.max_q * p.H_q;
   const dim3 join(static_cast<unsigned>((rows + 7) / 8));
