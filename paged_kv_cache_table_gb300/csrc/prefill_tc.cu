@@ -735,6 +735,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         continue;
       }
       const bool row_ok = tq0 + tok < it.t_end;
+      const bool live = __any_sync(0xffffffffu, row_ok);
       const int row_pos = it.first_pos + tq0 + tok;
       const int row_lo = p.window > 0 ? max(0, row_pos - p.window + 1) : 0;
       // position of this item's (part's) first column, window part, and the anchors from there on
@@ -754,15 +755,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // that cross a row's causal or window edge take the per-key mask, and within them only
         // the 32-key chunks that some row of the warp attends in part.  The masked chunks go back to
         // TMEM, so that one unrolled chunk of mask code serves all four: the tile loop has to
-        // stay small (see below).
-        if (!__all_sync(0xffffffffu, row_ok && kbase + 127 <= row_pos && kbase >= row_lo)) {
+        // stay small (see below).  Rows past the tile's tokens are not masked (nothing of them is
+        // stored), and a warp that has no others (!live) leaves its P as it finds it.
+        if (!__all_sync(0xffffffffu, !row_ok || (kbase + 127 <= row_pos && kbase >= row_lo))) {
           auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };  // columns < n
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
             const int c0 = kbase + 32 * q;
             uint32_t hide = below(row_lo - c0);
             if constexpr (ANCH) hide &= ~below(an0 - 128 * k - 32 * q);  // anchors
-            const uint32_t keep = row_ok ? below(row_pos - c0 + 1) & ~hide : 0u;
+            const uint32_t keep = row_ok ? below(row_pos - c0 + 1) & ~hide : ~0u;
             if (__all_sync(0xffffffffu, keep == ~0u)) continue;
             uint32_t v[32];
             tmem_ld32(tS + 32 * q, v);
@@ -784,7 +786,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         };
         uint32_t va[32], vb[32];
-        {
+        if (live) {
           uint32_t vc[32], vd[32];
           tmem_ld32(tS + 64, vc);
           tmem_ld32(tS + 96, vd);
@@ -846,7 +848,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tmem_st16(tS + 16 * h, pw);
         };
 #pragma unroll 1
-        for (int h = 0; h < 4; h += 2) {
+        for (int h = 0; live && h < 4; h += 2) {
           const uint32_t more = h == 0;
           chunk_exp(va, h);
           tmem_ld32_if(more, tS + 64, va);
