@@ -120,6 +120,13 @@ struct DecodeParams {
   int raw_ctx, raw_g;
 };
 
+// The parameters of a call without anchors: P below is either, and with this one their arithmetic is not in the
+// code (at run time it cost calls of 14 to 19 us 0.2 to 0.4).
+struct PlainDecode : DecodeParams {
+  static constexpr int anchors = 0;
+  explicit PlainDecode(const DecodeParams& p) : DecodeParams(p) {}
+};
+
 // Blocks of a sequence with ctx tokens; -1 for an invalid context.
 __device__ __forceinline__ int seq_blocks(const DecodeParams& p, int ctx) {
   if (ctx == 0) return 0;
@@ -129,7 +136,8 @@ __device__ __forceinline__ int seq_blocks(const DecodeParams& p, int ctx) {
 
 // First position of the query's window: the last `window` positions (ldpk §5.3), else 0; 0 too
 // when the anchors reach the window, since everything is then attended.
-__device__ __forceinline__ int window_lo(const DecodeParams& p, int ctx) {
+template <class P>
+__device__ __forceinline__ int window_lo(const P& p, int ctx) {
   const int lo = (p.window > 0 && ctx > p.window) ? ctx - p.window : 0;
   return lo <= p.anchors ? 0 : lo;
 }
@@ -140,7 +148,8 @@ __device__ __forceinline__ int window_lo(const DecodeParams& p, int ctx) {
 // holds the last anchors and the window's first positions is listed twice, once for either part:
 // the stage metadata (first, one past the last attended token) then needs no mask with a hole, and
 // the second load is an L2 hit.
-__device__ __forceinline__ int anchor_blocks(const DecodeParams& p, int lo) {
+template <class P>
+__device__ __forceinline__ int anchor_blocks(const P& p, int lo) {
   return (lo > 0 && p.anchors > p.num_sink)
              ? (p.anchors + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE - p.num_sink / PA_BLOCK_SIZE
              : 0;
@@ -151,20 +160,23 @@ __device__ __forceinline__ int anchor_blocks(const DecodeParams& p, int lo) {
 __device__ __forceinline__ bool shares_prefix(const DecodeParams& p, int s) {
   return p.shared_flags && p.shared_flags[s] == kSharedUse;
 }
-__device__ __forceinline__ int seq_lo(const DecodeParams& p, int s, int ctx) {
+template <class P>
+__device__ __forceinline__ int seq_lo(const P& p, int s, int ctx) {
   const int lo = window_lo(p, ctx);
   return shares_prefix(p, s) ? max(lo, min(p.shared_len, max(ctx, 0))) : lo;
 }
 
 // First logical block of a sequence's window part.  With anchors, blocks that hold sink positions only
 // are left out: they may have been released (their rows come from the sink buffers).
-__device__ __forceinline__ int window_block(const DecodeParams& p, int lo) {
+template <class P>
+__device__ __forceinline__ int window_block(const P& p, int lo) {
   return (p.anchors > 0 ? max(lo, p.num_sink) : lo) / PA_BLOCK_SIZE;
 }
 
 // Logical blocks a sequence's query visits (those holding positions seq_lo .. ctx-1, and its
 // anchors'); -1 for an invalid context.
-__device__ __forceinline__ int seq_span(const DecodeParams& p, int s, int ctx) {
+template <class P>
+__device__ __forceinline__ int seq_span(const P& p, int s, int ctx) {
   const int nb = seq_blocks(p, ctx);
   if (nb <= 0) return nb;
   const int lo = seq_lo(p, s, ctx);
@@ -749,21 +761,25 @@ struct Producer {
   bool waited;
 
   // whether list entry u of sequence s is one of its anchors' blocks
-  static __device__ __forceinline__ bool is_anchor(const DecodeParams& p, const Smem& sm, int s, int u) {
+  template <class P>
+  static __device__ __forceinline__ bool is_anchor(const P& p, const Smem& sm, int s, int u) {
     return u - sm.cum[s] < anchor_blocks(p, sm.los[s]);
   }
   // logical block of list entry u of sequence s (the anchors' blocks, then the window's)
-  static __device__ __forceinline__ int logical(const DecodeParams& p, const Smem& sm, int s, int u) {
+  template <class P>
+  static __device__ __forceinline__ int logical(const P& p, const Smem& sm, int s, int u) {
     const int i = u - sm.cum[s], na = anchor_blocks(p, sm.los[s]);
     return i < na ? p.num_sink / PA_BLOCK_SIZE + i : window_block(p, sm.los[s]) + i - na;
   }
-  static __device__ __forceinline__ int load_entry(const DecodeParams& p, const Smem& sm, const Range& r, int u) {
+  template <class P>
+  static __device__ __forceinline__ int load_entry(const P& p, const Smem& sm, const Range& r, int u) {
     if (u >= r.u1) return -1;
     const int s = find_seq(sm.cum, r.nseq, u);
     return p.block_tables[static_cast<size_t>(r.seq_base + s) * p.max_blocks + logical(p, sm, s, u)];
   }
 
-  __device__ __forceinline__ void init(const DecodeParams& p, const Smem& sm, const Range& r, int lane, bool step) {
+  template <class P>
+  __device__ __forceinline__ void init(const P& p, const Smem& sm, const Range& r, int lane, bool step) {
     waited = !step;
     base = r.u0;
     cur_pb = load_entry(p, sm, r, base + lane);
@@ -771,7 +787,8 @@ struct Producer {
     pack(p, sm, r, lane, step);
   }
 
-  __device__ __forceinline__ void pack(const DecodeParams& p, const Smem& sm, const Range& r, int lane, bool step) {
+  template <class P>
+  __device__ __forceinline__ void pack(const P& p, const Smem& sm, const Range& r, int lane, bool step) {
     const int u = base + lane;
     const bool valid = u < r.u1;
     const int s = valid ? find_seq(sm.cum, r.nseq, u) : 0;
@@ -793,7 +810,8 @@ struct Producer {
   }
 
   // Fill the stage of iteration k (its previous use must have been released).
-  __device__ __forceinline__ void issue(const DecodeParams& p, const Smem& sm, const Range& r, int lane, bool step,
+  template <class P>
+  __device__ __forceinline__ void issue(const P& p, const Smem& sm, const Range& r, int lane, bool step,
                                         int hgi, int k, const CUtensorMap* tmK, const CUtensorMap* tmV,
                                         const CUtensorMap* tmKp, const CUtensorMap* tmVp) {
     const int S = p.stages, nbs = p.nbs;
@@ -854,11 +872,11 @@ __device__ __forceinline__ void drain_copies(const Smem& sm, int S, int from, in
   }
 }
 
-template <int D, int KIND, int MAXW, bool WT = false>
+template <int D, int KIND, int MAXW, bool WT = false, class P = DecodeParams>
 __global__ void __launch_bounds__((MAXW + 1) * 32, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const __grid_constant__ CUtensorMap tmKp, const __grid_constant__ CUtensorMap tmVp,
-                  const DecodeParams p) {
+                  const P p) {
   extern __shared__ uint8_t smem_raw[];
   const Smem sm = carve(smem_raw, p);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1100,8 +1118,8 @@ struct SinkRow {
   }
 };
 
-template <int D, int WPR, int CH>
-__device__ __forceinline__ void merge_rows(const DecodeParams& p, int grid_x) {
+template <int D, int WPR, int CH, class P>
+__device__ __forceinline__ void merge_rows(const P& p, int grid_x) {
   constexpr int E = D / 32;  // dims per lane
   const int s = blockIdx.x;
   const int wid = threadIdx.x >> 5;
@@ -1283,8 +1301,8 @@ __device__ __forceinline__ void merge_rows(const DecodeParams& p, int grid_x) {
   for (int e = 0; e < E; ++e) orow[lane * E + e] = __float2bfloat16_rn(acc[e] * inv);
 }
 
-template <int D, int WPR, int CH>
-__global__ void __launch_bounds__(128) merge_kernel(const DecodeParams p, int grid_x) {
+template <int D, int WPR, int CH, class P>
+__global__ void __launch_bounds__(128) merge_kernel(const P p, int grid_x) {
   merge_rows<D, WPR, CH>(p, grid_x);
 }
 
@@ -1615,30 +1633,30 @@ pa_status launch_weights_tail(const Plan& pl, const DecodeParams& p, const Weigh
 template <int D, int KIND>
 pa_status launch_weights(const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mkp,
                          const CUtensorMap& mvp, const DecodeParams& p, WeightsParams wp, cudaStream_t stream) {
-  auto kern = decode_kernel<D, KIND, 8, true>;
+  auto kern = decode_kernel<D, KIND, 8, true, PlainDecode>;
   if (pl.warps_c > 8) {
     if constexpr (KIND == 2) return PA_ERR_UNSUPPORTED;  // 4-bit plans have at most 8 consumer warps
-    else kern = decode_kernel<D, KIND, kMaxConsumerWarps, true>;
+    else kern = decode_kernel<D, KIND, kMaxConsumerWarps, true, PlainDecode>;
   }
   if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kern), pl.smem_bytes)) return PA_ERR_CUDA;
   const dim3 grid = p.mode == 0 ? dim3(pl.grid_x, pl.n_hg, 1) : dim3(pl.max_parts, p.B, pl.n_hg);
-  if (launch_overlapped(kern, grid, dim3(pl.threads), pl.smem_bytes, stream, mk, mv, mkp, mvp, p) != PA_OK)
+  if (launch_overlapped(kern, grid, dim3(pl.threads), pl.smem_bytes, stream, mk, mv, mkp, mvp, PlainDecode(p)) != PA_OK)
     return PA_ERR_CUDA;
   const bool few = static_cast<long long>(p.B) * p.H_q < 4LL * std::max(1, sm_count_current());
   wp.merge_y = few ? p.H_q : (p.H_q + 3) / 4;
   return few ? launch_weights_tail<D, 4>(pl, p, wp, stream) : launch_weights_tail<D, 1>(pl, p, wp, stream);
 }
 
-template <int D, int KIND>
-pa_status launch(const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mkp,
-                 const CUtensorMap& mvp, const DecodeParams& p, cudaStream_t stream) {
+template <int D, int KIND, class P>
+pa_status launch_as(const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mkp,
+                 const CUtensorMap& mvp, const P& p, cudaStream_t stream) {
   // 9-warp CTAs get the register budget of a 288-thread launch; wider ones a 416-thread (INT4
   // only: four warps per scheduler, 128 registers) or a 544-thread one
-  auto kern = decode_kernel<D, KIND, kMaxConsumerWarps>;
+  auto kern = decode_kernel<D, KIND, kMaxConsumerWarps, false, P>;
   if (pl.warps_c <= 8) {
-    kern = decode_kernel<D, KIND, 8>;
+    kern = decode_kernel<D, KIND, 8, false, P>;
   } else if constexpr (KIND == 2) {
-    if (pl.warps_c <= 12) kern = decode_kernel<D, KIND, 12>;
+    if (pl.warps_c <= 12) kern = decode_kernel<D, KIND, 12, false, P>;
   }
   if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kern), pl.smem_bytes)) return PA_ERR_CUDA;
   const dim3 grid = p.mode == 0 ? dim3(pl.grid_x, pl.n_hg, 1) : dim3(pl.max_parts, p.B, pl.n_hg);
@@ -1648,12 +1666,19 @@ pa_status launch(const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, c
     return PA_ERR_CUDA;
   // few (sequence, head) rows for the SMs (long contexts, small batches): four warps per row
   if (static_cast<long long>(p.B) * p.H_q < 4LL * std::max(1, sm_count_current()) && p.anchors > 0)
-    return launch_overlapped(merge_kernel<D, 4, 16>, dim3(p.B, p.H_q), dim3(128), 0, stream, p, pl.grid_x);
+    return launch_overlapped(merge_kernel<D, 4, 16, P>, dim3(p.B, p.H_q), dim3(128), 0, stream, p, pl.grid_x);
   if (static_cast<long long>(p.B) * p.H_q < 4LL * std::max(1, sm_count_current()))
-    return launch_overlapped(merge_kernel<D, 4, 8>, dim3(p.B, p.H_q), dim3(128), 0, stream, p, pl.grid_x);
+    return launch_overlapped(merge_kernel<D, 4, 8, P>, dim3(p.B, p.H_q), dim3(128), 0, stream, p, pl.grid_x);
   if (p.n_extra > 0)
-    return launch_overlapped(merge_kernel<D, 1, 16>, dim3(p.B, (p.H_q + 3) / 4), dim3(128), 0, stream, p, pl.grid_x);
-  return launch_overlapped(merge_kernel<D, 1, 8>, dim3(p.B, (p.H_q + 3) / 4), dim3(128), 0, stream, p, pl.grid_x);
+    return launch_overlapped(merge_kernel<D, 1, 16, P>, dim3(p.B, (p.H_q + 3) / 4), dim3(128), 0, stream, p, pl.grid_x);
+  return launch_overlapped(merge_kernel<D, 1, 8, P>, dim3(p.B, (p.H_q + 3) / 4), dim3(128), 0, stream, p, pl.grid_x);
+}
+
+template <int D, int KIND>
+pa_status launch(const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mkp,
+                 const CUtensorMap& mvp, const DecodeParams& p, cudaStream_t stream) {
+  return p.anchors > 0 ? launch_as<D, KIND>(pl, mk, mv, mkp, mvp, p, stream)
+                       : launch_as<D, KIND>(pl, mk, mv, mkp, mvp, PlainDecode(p), stream);
 }
 
 }  // namespace
