@@ -45,7 +45,8 @@
 //    when the maximum moved rescale O in TMEM before handing any of P over (O is complete by
 //    then: its P·V was issued before this S).  V rows of keys that are not loaded or lie beyond
 //    the context are zeroed before P·V reads them, so bits left in unused slots (NaN included)
-//    cannot leak.
+//    cannot leak.  The code of a tile is kept small (rolled chunks), because it is fetched anew
+//    for every tile; rows past the tile's tokens are computed without masks and not stored.
 //  * Anchors (pa_prefill_attention_anchored; ANCH, a template parameter, so that the plain kernel
 //    carries none of it): the first A positions stay visible beside the window.  An item lists the
 //    anchors' blocks and then its window's as one sequence of blocks, cut into tiles of 8, so four
