@@ -832,7 +832,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // maximum moved, O is rescaled before P is handed over.  Two chunks of 32 keys are unrolled and
         // gone through twice, the second two loaded meanwhile: with all 128 scores in registers and
         // everything unrolled the loop outgrows the instruction cache and spills (8 x 512 queries over
-        // 4096 keys 255 us, now 227; 6 chunks of up to 700 over 1000 128 us, now 113).
+        // 4096 keys 255 us, with the last round in parts now 232; 6 chunks of up to 700 over 1000 128 us, now 110).
         float ls4[4] = {0.f, 0.f, 0.f, 0.f};
         auto chunk_exp = [&](const uint32_t (&v)[32], int h) {
           uint32_t pw[16];
