@@ -736,7 +736,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         continue;
       }
       const bool row_ok = tq0 + tok < it.t_end;
-      const bool live = __any_sync(0xffffffffu, row_ok);
       const int row_pos = it.first_pos + tq0 + tok;
       const int row_lo = p.window > 0 ? max(0, row_pos - p.window + 1) : 0;
       // position of this item's (part's) first column, window part, and the anchors from there on
@@ -756,8 +755,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // that cross a row's causal or window edge take the per-key mask, and within them only
         // the 32-key chunks that some row of the warp attends in part.  The masked chunks go back to
         // TMEM, so that one unrolled chunk of mask code serves all four: the tile loop has to
-        // stay small (see below).  Rows past the tile's tokens are not masked (nothing of them is
-        // stored), and a warp that has no others (!live) leaves its P as it finds it.
+        // stay small (see below).  Rows past the tile's tokens are not masked: nothing of them is
+        // stored (skipping all work of a warp without others cost the full tiles 2 %).
         if (!__all_sync(0xffffffffu, !row_ok || (kbase + 127 <= row_pos && kbase >= row_lo))) {
           auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };  // columns < n
 #pragma unroll 1
@@ -787,7 +786,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         };
         uint32_t va[32], vb[32];
-        if (live) {
+        {
           uint32_t vc[32], vd[32];
           tmem_ld32(tS + 64, vc);
           tmem_ld32(tS + 96, vd);
@@ -832,7 +831,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // maximum moved, O is rescaled before P is handed over.  Two chunks of 32 keys are unrolled and
         // gone through twice, the second two loaded meanwhile: with all 128 scores in registers and
         // everything unrolled the loop outgrows the instruction cache and spills (8 x 512 queries over
-        // 4096 keys 255 us, with the last round in parts now 232; 6 chunks of up to 700 over 1000 128 us, now 110).
+        // 4096 keys 255 us, with the last round in parts now 227; 6 chunks of up to 700 over 1000 128 us, now 107).
         float ls4[4] = {0.f, 0.f, 0.f, 0.f};
         auto chunk_exp = [&](const uint32_t (&v)[32], int h) {
           uint32_t pw[16];
@@ -849,7 +848,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tmem_st16(tS + 16 * h, pw);
         };
 #pragma unroll 1
-        for (int h = 0; live && h < 4; h += 2) {
+        for (int h = 0; h < 4; h += 2) {
           const uint32_t more = h == 0;
           chunk_exp(va, h);
           tmem_ld32_if(more, tS + 64, va);
